@@ -440,6 +440,154 @@ smla_status smla_indexer_select(const float *scores, const int32_t *n_vis, int B
                                 int max_n, int K, void *workspace, size_t workspace_bytes,
                                 int32_t *topk_idx, void *stream);
 
+/*
+ * The 4-bit latent cache.
+ *
+ * Serving keeps the latent rows of every token of every sequence resident; at
+ * 1152 bytes a row that is what bounds the batch, and reading the rows is what
+ * bounds the decode.  The 4-bit cache holds a row in 416 bytes:
+ *
+ *   bytes [0, 256)    codes of the 512 latents, 4 bits each
+ *   bytes [256, 288)  16 bf16 scales, one per 32 latents
+ *   bytes [288, 416)  the 64 rope values in bf16, unchanged
+ *
+ * Latent d reads back as (code[d] - 8) * scale[d / 32], which is always a bf16
+ * number.  scale is the smallest number of four significant bits that is at
+ * least max|x| / 7 over the 32 latents; code - 8 in [-7, 7] is x / scale
+ * rounded to the nearest integer, ties to even.  Eight codes share a
+ * little-endian 32-bit word: nibble k < 4 is value 2 k of the eight, nibble
+ * k + 4 value 2 k + 1.  A group whose magnitudes are all below 2^-118 is stored
+ * as zeros.  A row with a latent that is NaN or of magnitude 2^120 or more
+ * (infinities too) has zeros in that group and NaN in all its rope values, so
+ * that every query token which attends to it, and no other, gets NaN.
+ * The cache is paged as the bf16 one: uint8 [num_pages, 64, 416], 16-B
+ * aligned, and position i of sequence b is row
+ * page_table[b * pt_stride + i / 64] * 64 + i % 64.
+ *
+ * smla_q4_append quantises new rows and writes them behind what the sequences
+ * hold: rows [cu_rows[b], cu_rows[b + 1]) go to positions start[b],
+ * start[b] + 1, ... of sequence b.  A decode step has one row per sequence, a
+ * prompt many; both may share a call.
+ *
+ *   rows     bf16  [n_rows, 576]   device, 16-B aligned
+ *   cu_rows  int32 [B + 1]         device, ascending from 0; rows at or behind
+ *                                  cu_rows[B] belong to no sequence and are
+ *                                  left out
+ *   start    int32 [B]             device
+ * A row whose position no page maps, or that a cu_rows which is not ascending
+ * gives to no sequence, is not written and is counted (SMLA_ERR_INDEX_RANGE in
+ * smla_check_device).  No two sequences of one call may own the same page
+ * entry for the positions they write.
+ *
+ * smla_q4_read gathers rows back as bf16 [B, K, 576]: entry (b, j) is position
+ * positions[b * K + j] of sequence b.  -1 gives a row of zeros; so does a
+ * position that no page maps, which is counted.
+ */
+#define SMLA_Q4_ROW_BYTES 416
+smla_status smla_q4_append(const void *rows, int n_rows, const int32_t *cu_rows, const int32_t *start,
+                           int B, void *cache_q4, int64_t num_pages, const int32_t *page_table,
+                           int pt_stride, int page_size, void *stream);
+smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t *page_table, int pt_stride,
+                         const int32_t *positions, int B, int K, int page_size, void *rows, void *stream);
+
+/*
+ * Decode over the 4-bit cache.  smla_decode_q4 is smla_decode and
+ * smla_decode_dense_q4 is smla_decode_dense with the rows read from a 4-bit
+ * cache: same definition (on the values the cache holds), layouts, index
+ * conventions, clamping and errors.  o is rounded to bf16 once per output (and
+ * each probability once, as in the bf16 decode); the decoded latents are exact.
+ *   nsplit  0 picks smla_q4_nsplit(B, T, H, K), smla_dense_q4_nsplit(B, T, H, K)
+ *   workspace_bytes  at least smla_workspace_bytes(B, T, H, nsplit) (nothing
+ *           for nsplit 1), or smla_dense_q4_workspace_bytes(B, T, H, K, nsplit),
+ *           for the nsplit used; else SMLA_ERR_WORKSPACE_TOO_SMALL
+ * K above SMLA_MAX_K gives SMLA_ERR_INVALID_ARG.  Calls that may overlap on the
+ * GPU, two captured graphs among them, need a workspace each.
+ */
+int smla_q4_nsplit(int B, int T, int H, int K);
+smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                           const int32_t *page_table, int pt_stride, const int32_t *topk_idx, int B,
+                           int T, int H, int K, int page_size, float scale, int nsplit, void *workspace,
+                           size_t workspace_bytes, void *o, float *lse, void *stream);
+int smla_dense_q4_nsplit(int B, int T, int H, int K);
+size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit);
+smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                                 const int32_t *page_table, int pt_stride, const int32_t *seq_lens, int B,
+                                 int T, int H, int K, int page_size, float scale, int nsplit,
+                                 void *workspace, size_t workspace_bytes, void *o, float *lse,
+                                 void *stream);
+
+/*
+ * Eviction by accumulated attention weight.
+ *
+ * A sequence that has outgrown its share of the cache gives up the rows that
+ * received the least attention.  Three steps, each its own entry point.
+ *
+ * 1. smla_evict_accumulate (smla_evict_accumulate_q4 for the 4-bit cache) adds
+ *    the attention weight that a decode's query tokens gave to each position:
+ *      acc[b, i] += sum over (t, h) with i < seq_lens[b, t] of
+ *                   exp(scale * q[b,t,h] . row_i - lse[b,t,h])
+ *    for the q, seq_lens and lse of a dense decode over the same cache.  The
+ *    sum is fp32 in a fixed order: repeated calls give the same bits.
+ *      acc  fp32 [B, max_n]  device; positions no query token sees stay as
+ *                            they are, and so does a position that no page
+ *                            maps (counted)
+ *    A length outside [0, max_n] is clamped and counted.  A query row with
+ *    lse = -inf (it attended to nothing) adds nothing.
+ *
+ * 2. smla_evict_plan chooses, for each sequence of n[b] slots, the
+ *    m = min(n[b], K) that stay, and which row each slot gets:
+ *      pos  int32 [B, max_n], or NULL: the original position of the token in
+ *           slot i (NULL: i).  Tokens with pos < n_sink, and those with
+ *           pos >= (largest pos) + 1 - n_recent, stay whatever their weight;
+ *           n_sink + n_recent <= K.
+ *      The others rank by acc, larger first; NaN counts as -inf; equal weights
+ *      go to the smaller slot.
+ *      src  int32 [B, K]: slot i < m takes the row of slot src[b, i].  A slot
+ *           below m whose token stays keeps it (src = i); the j-th slot below m
+ *           whose token leaves takes the j-th staying token at or behind m.
+ *           So only the rows that fill holes move, every source lies at or
+ *           behind m and every destination before it, and the order of the
+ *           slots carries no meaning afterwards: pos does.  -1 from m on.
+ *      n_new int32 [B]: m.
+ *      acc_new fp32, pos_new int32 [B, max_n], either may be NULL: acc and pos
+ *           carried along (slot i from src[b, i]); 0 and -1 from m on.
+ *    acc_new, pos_new and n_new must not overlap acc, pos and n
+ *    (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
+ *    outside [0, max_n] is clamped and counted.  workspace: device, 16-B
+ *    aligned, at least smla_evict_workspace_bytes(B, max_n).
+ *
+ * 3. smla_evict_apply moves the rows, in place, in up to SMLA_EVICT_MAX_CACHES
+ *    paged buffers that share the page table: for every i with src[b, i] not
+ *    -1 and not i, row src[b, i] of sequence b is copied to row i.
+ *      caches    host array of n_caches device pointers, [num_pages, 64,
+ *                row_bytes[k]] bytes each, 16-B aligned
+ *      row_bytes host array: multiples of 16 up to SMLA_EVICT_MAX_ROW_BYTES
+ *                (1152 for the bf16 latent cache, 416 for the 4-bit one, 256
+ *                for the index keys)
+ *    With a src that smla_evict_plan wrote the moves are independent, and
+ *    applying them twice changes nothing.  An entry whose source or destination
+ *    no page maps is left out and counted.  Pages must not be shared with
+ *    another sequence.
+ */
+#define SMLA_EVICT_MAX_N 524288
+#define SMLA_EVICT_MAX_CACHES 4
+#define SMLA_EVICT_MAX_ROW_BYTES 65536
+smla_status smla_evict_accumulate(const void *q, const void *kv_cache, int64_t num_pages,
+                                  const int32_t *page_table, int pt_stride, const int32_t *seq_lens,
+                                  const float *lse, int B, int T, int H, int page_size, float scale,
+                                  float *acc, int max_n, void *stream);
+smla_status smla_evict_accumulate_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                                     const int32_t *page_table, int pt_stride, const int32_t *seq_lens,
+                                     const float *lse, int B, int T, int H, int page_size, float scale,
+                                     float *acc, int max_n, void *stream);
+size_t smla_evict_workspace_bytes(int B, int max_n);
+smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t *n, int B, int max_n, int K,
+                            int n_sink, int n_recent, void *workspace, size_t workspace_bytes,
+                            int32_t *src, int32_t *n_new, float *acc_new, int32_t *pos_new, void *stream);
+smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *page_table, int pt_stride,
+                             int64_t num_pages, int page_size, void *const *caches, const int32_t *row_bytes,
+                             int n_caches, void *stream);
+
 /* Static text for a status code. */
 const char *smla_status_string(smla_status status);
 

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -60,6 +60,21 @@ SIGNATURES = {
                                  _P]),
     "smla_indexer_select": (_I, [_P, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "smla_indexer_select_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "smla_q4_append": (_I, [_P, _I, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
+    "smla_q4_read": (_I, [_P, _I64, _P, _I, _P, _I, _I, _I, _P, _P]),
+    "smla_q4_nsplit": (_I, [_I, _I, _I, _I]),
+    "smla_decode_q4": (_I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _P,
+                            _P]),
+    "smla_dense_q4_nsplit": (_I, [_I, _I, _I, _I]),
+    "smla_dense_q4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "smla_decode_dense_q4": (_I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P,
+                                  _P, _P]),
+    "smla_evict_accumulate": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _I, _P]),
+    "smla_evict_accumulate_q4": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _I,
+                                      _P]),
+    "smla_evict_workspace_bytes": (_SZ, [_I, _I]),
+    "smla_evict_plan": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P, _P, _P, _P, _P]),
+    "smla_evict_apply": (_I, [_P, _I, _I, _P, _I, _I64, _I, _P, _P, _I, _P]),
     "smla_selftest_wait_timeout": (_I, [ctypes.c_ulonglong, _P]),
     "smla_check_device": (_I, [_I, ctypes.POINTER(ctypes.c_ulonglong), _P]),
     "smla_status_string": (ctypes.c_char_p, [_I]),
@@ -467,6 +482,275 @@ def indexer_select(scores, n_vis, K: int, *, out=None, workspace=None, stream=No
                                      _ptr(workspace), workspace.numel(), _ptr(out),
                                      _stream(stream)), "smla_indexer_select")
     return out
+
+
+# ---------------------------------------------------------------- 4-bit latent cache
+Q4_ROW_BYTES = 416
+
+
+def _launch(name, dev, stream, *args):
+    """Call an entry point with the tensors' device current, on ``stream`` or on
+    that device's current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(name, dev, stream, *args)
+    _check(getattr(lib(), name)(*args, _stream(stream)), name)
+
+
+def _new(shape, dtype, dev, stream):
+    """An empty tensor that a launch on ``stream`` uses: the allocator keeps its
+    memory from other streams until that launch is done, should it be dropped
+    before."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+        t.record_stream(stream)
+    return t
+
+
+def _pages_of(cache, width, what):
+    """Number of pages of a paged cache tensor [num_pages, 64, width]."""
+    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or cache.shape[2] != width:
+        raise ValueError(f"{what} must be [num_pages, {PAGE_SIZE}, {width}], got {list(cache.shape)}")
+    return cache.shape[0]
+
+
+def _table(page_table, B, device):
+    _need(page_table, torch.int32, "page_table", device)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, pt_stride]")
+    return page_table.shape[1]
+
+
+def q4_append(rows, cache, page_table, cu_rows, start, *, stream=None):
+    """Quantise new latent rows into the 4-bit cache: rows [cu_rows[b],
+    cu_rows[b + 1]) of ``rows`` (bf16 [N, 576]) go to positions start[b],
+    start[b] + 1, ... of sequence b.  cache is uint8 [num_pages, 64, 416],
+    cu_rows int32 [B + 1], start int32 [B]; rows at or behind cu_rows[B] are
+    left out.  Writes into cache and returns it."""
+    _need(rows, torch.bfloat16, "rows")
+    dev = rows.device
+    if rows.dim() != 2 or rows.shape[1] != D:
+        raise ValueError(f"rows must be [N, {D}]")
+    _need(start, torch.int32, "start", dev)
+    if start.dim() != 1:
+        raise ValueError("start must be [B]")
+    B = start.shape[0]
+    _need(cu_rows, torch.int32, "cu_rows", dev, (B + 1,))
+    _need(cache, torch.uint8, "cache", dev)
+    num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
+    pt_stride = _table(page_table, B, dev)
+    _launch("smla_q4_append", dev, stream, _ptr(rows), _k_in_range(rows.shape[0]), _ptr(cu_rows),
+            _ptr(start), B, _ptr(cache), num_pages, _ptr(page_table), pt_stride, PAGE_SIZE)
+    return cache
+
+
+def q4_read(cache, page_table, positions, *, out=None, stream=None):
+    """Rows of the 4-bit cache as bf16 [B, K, 576]: entry (b, j) is position
+    positions[b, j] of sequence b (int32 [B, K]; -1 gives zeros)."""
+    _need(cache, torch.uint8, "cache")
+    dev = cache.device
+    num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
+    _need(positions, torch.int32, "positions", dev)
+    if positions.dim() != 2:
+        raise ValueError("positions must be [B, K]")
+    B, K = positions.shape
+    pt_stride = _table(page_table, B, dev)
+    if out is None:
+        out = _new((B, K, D), torch.bfloat16, dev, stream)
+    _need(out, torch.bfloat16, "out", dev, (B, K, D))
+    _launch("smla_q4_read", dev, stream, _ptr(cache), num_pages, _ptr(page_table), pt_stride,
+            _ptr(positions), B, _k_in_range(K), PAGE_SIZE, _ptr(out))
+    return out
+
+
+def q4_nsplit(B: int, T: int, H: int, K: int) -> int:
+    return int(lib().smla_q4_nsplit(B, T, H, _k_in_range(K)))
+
+
+def dense_q4_nsplit(B: int, T: int, H: int, K: int) -> int:
+    return int(lib().smla_dense_q4_nsplit(B, T, H, _k_in_range(K)))
+
+
+def dense_q4_workspace_bytes(B: int, T: int, H: int, K: int, nsplit: int) -> int:
+    return int(lib().smla_dense_q4_workspace_bytes(B, T, H, _k_in_range(K), nsplit))
+
+
+def _q4_decode_args(q, cache, page_table):
+    _need(q, torch.bfloat16, "q")
+    dev = q.device
+    if q.dim() != 4 or q.shape[-1] != D:
+        raise ValueError(f"q must be [B,T,H,{D}]")
+    B, T, H, _ = q.shape
+    _need(cache, torch.uint8, "cache", dev)
+    return dev, B, T, H, _pages_of(cache, Q4_ROW_BYTES, "cache"), _table(page_table, B, dev)
+
+
+def _decode_out(dev, B, T, H, need, workspace, o, lse, stream):
+    """Workspace and outputs of a decode, allocated where they are not given."""
+    if workspace is None:
+        workspace = _new(max(need, 16), torch.uint8, dev, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace", dev)
+    if o is None:
+        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
+    else:
+        _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
+    if lse is None:
+        lse = _new((B, T, H), torch.float32, dev, stream)
+    else:
+        _need(lse, torch.float32, "lse", dev, (B, T, H))
+    return workspace, o, lse
+
+
+def decode_q4(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, workspace=None, o=None,
+              lse=None, stream=None):
+    """decode() over a 4-bit cache (uint8 [num_pages, 64, 416], as q4_append
+    writes it); returns (o bf16 [B,T,H,512], lse fp32 [B,T,H])."""
+    dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
+    _need(idx, torch.int32, "idx", dev)
+    if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, T):
+        raise ValueError("idx must be [B,T,K]")
+    K = _k_in_range(idx.shape[2])
+    if nsplit == 0:
+        nsplit = q4_nsplit(B, T, H, K)
+    need = workspace_bytes(B, T, H, nsplit) if nsplit > 1 else 0
+    workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
+    _launch("smla_decode_q4", dev, stream, _ptr(q), _ptr(cache), num_pages, _ptr(page_table),
+            pt_stride, _ptr(idx), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit), _ptr(workspace),
+            workspace.numel(), _ptr(o), _ptr(lse))
+    return o, lse
+
+
+def decode_dense_q4(q, cache, page_table, seq_lens, scale: float, nsplit: int = 0, *, K=None,
+                    workspace=None, o=None, lse=None, stream=None):
+    """decode_dense() over a 4-bit cache: query token (b, t) attends to
+    positions 0 .. seq_lens[b, t] - 1 of sequence b.  K defaults to the longest
+    length (read from seq_lens, which synchronises)."""
+    dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    if tuple(seq_lens.shape) != (B, T):
+        raise ValueError("seq_lens must be [B,T]")
+    if K is None:
+        K = int(seq_lens.max().item()) if seq_lens.numel() else 0
+    K = _k_in_range(int(K))
+    if nsplit == 0:
+        nsplit = dense_q4_nsplit(B, T, H, K)
+    need = dense_q4_workspace_bytes(B, T, H, K, nsplit)
+    workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
+    _launch("smla_decode_dense_q4", dev, stream, _ptr(q), _ptr(cache), num_pages, _ptr(page_table),
+            pt_stride, _ptr(seq_lens), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit),
+            _ptr(workspace), workspace.numel(), _ptr(o), _ptr(lse))
+    return o, lse
+
+
+# ---------------------------------------------------------------- eviction
+EVICT_MAX_N, EVICT_MAX_CACHES, EVICT_MAX_ROW_BYTES = 524288, 4, 65536
+
+
+class EvictPlan(NamedTuple):
+    """What evict_plan returns: src int32 [B, K] (slot i takes the row of slot
+    src[b, i]; -1 past the end), n int32 [B] (slots in use afterwards), acc and
+    pos [B, max_n] carried along."""
+    src: torch.Tensor
+    n: torch.Tensor
+    acc: torch.Tensor
+    pos: torch.Tensor
+
+
+def evict_workspace_bytes(B: int, max_n: int) -> int:
+    return int(lib().smla_evict_workspace_bytes(B, max_n))
+
+
+def evict_accumulate(q, cache, page_table, seq_lens, lse, scale: float, acc, *, stream=None):
+    """Add to acc (fp32 [B, max_n], in place) the attention weight that the
+    query tokens of a dense decode gave to each position: q, seq_lens and lse
+    are that decode's.  cache is the bf16 or the 4-bit latent cache.  Returns
+    acc."""
+    _need(q, torch.bfloat16, "q")
+    dev = q.device
+    if q.dim() != 4 or q.shape[-1] != D:
+        raise ValueError(f"q must be [B,T,H,{D}]")
+    B, T, H, _ = q.shape
+    q4 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
+    _need(cache, torch.uint8 if q4 else torch.bfloat16, "cache", dev)
+    num_pages = _pages_of(cache, Q4_ROW_BYTES if q4 else D, "cache")
+    pt_stride = _table(page_table, B, dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev, (B, T))
+    _need(lse, torch.float32, "lse", dev, (B, T, H))
+    _need(acc, torch.float32, "acc", dev)
+    if acc.dim() != 2 or acc.shape[0] != B:
+        raise ValueError("acc must be [B, max_n]")
+    _launch("smla_evict_accumulate_q4" if q4 else "smla_evict_accumulate", dev, stream, _ptr(q),
+            _ptr(cache), num_pages, _ptr(page_table), pt_stride, _ptr(seq_lens), _ptr(lse), B, T, H,
+            PAGE_SIZE, float(scale), _ptr(acc), _k_in_range(acc.shape[1]))
+    return acc
+
+
+def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, src=None, n_new=None,
+               acc_new=None, pos_new=None, workspace=None, stream=None) -> EvictPlan:
+    """Choose the min(n[b], K) slots of each sequence that stay, by accumulated
+    weight acc (fp32 [B, max_n]), and which row each slot takes.  pos (int32
+    [B, max_n], default: the slot's number) is the token's original position:
+    the first n_sink and the last n_recent always stay.  acc and pos come back
+    carried along to the new slots; the inputs are left as they are."""
+    _need(acc, torch.float32, "acc")
+    dev = acc.device
+    if acc.dim() != 2:
+        raise ValueError("acc must be [B, max_n]")
+    B, max_n = acc.shape
+    K = _k_in_range(int(K))
+    if K < 1:
+        raise ValueError("K must be at least 1")
+    _need(n, torch.int32, "n", dev, (B,))
+    if pos is not None:
+        _need(pos, torch.int32, "pos", dev, (B, max_n))
+    outs = []
+    for t, name, dtype, shape in ((src, "src", torch.int32, (B, K)), (n_new, "n_new", torch.int32, (B,)),
+                                  (acc_new, "acc_new", torch.float32, (B, max_n)),
+                                  (pos_new, "pos_new", torch.int32, (B, max_n))):
+        if t is None:
+            t = _new(shape, dtype, dev, stream)
+        else:
+            _need(t, dtype, name, dev, shape)
+        outs.append(t)
+    src, n_new, acc_new, pos_new = outs
+    if workspace is None:
+        workspace = _new(max(16, evict_workspace_bytes(B, max_n)), torch.uint8, dev, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace", dev)
+    _launch("smla_evict_plan", dev, stream, _ptr(acc), _ptr(pos), _ptr(n), B, max_n, K, int(n_sink),
+            int(n_recent), _ptr(workspace), workspace.numel(), _ptr(src), _ptr(n_new),
+            _ptr(acc_new), _ptr(pos_new))
+    return EvictPlan(src, n_new, acc_new, pos_new)
+
+
+def evict_apply(src, page_table, caches, *, stream=None):
+    """Move the rows of a plan, in place, in every paged buffer of ``caches``
+    (contiguous CUDA tensors [num_pages, 64, W] of any dtype, rows of a
+    multiple of 16 bytes, one page table for all): the bf16 or 4-bit latent
+    cache, the index keys.  Returns caches."""
+    _need(src, torch.int32, "src")
+    dev = src.device
+    if src.dim() != 2:
+        raise ValueError("src must be [B, K]")
+    B, K = src.shape
+    pt_stride = _table(page_table, B, dev)
+    if not 1 <= len(caches) <= EVICT_MAX_CACHES:
+        raise ValueError(f"caches must be 1 to {EVICT_MAX_CACHES} tensors")
+    ptrs, sizes, num_pages = (_P * len(caches))(), (ctypes.c_int32 * len(caches))(), None
+    for k, t in enumerate(caches):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("caches must be torch.Tensors")
+        _need(t, t.dtype, f"caches[{k}]", dev)
+        if t.dim() != 3 or t.shape[1] != PAGE_SIZE or t.shape[0] != caches[0].shape[0]:
+            raise ValueError(f"caches[{k}] must be [num_pages, {PAGE_SIZE}, width], the same pages in all")
+        num_pages, ptrs[k], sizes[k] = t.shape[0], t.data_ptr(), t.shape[2] * t.element_size()
+    _check(lib().smla_evict_apply(_ptr(src), B, _k_in_range(K), _ptr(page_table), pt_stride, num_pages,
+                                  PAGE_SIZE, ptrs, sizes, len(caches), _stream(stream)),
+           "smla_evict_apply")
+    return caches
 
 
 def check_device(clear: bool = True, stream=None):

@@ -27,6 +27,7 @@
 #include "smla_partial_mma.cuh"
 #include "smla_partial_tc.cuh"
 #include "smla_indexer.cuh"
+#include "smla_evict.cuh"
 
 namespace {
 
@@ -41,6 +42,8 @@ smla_status cuda_fail(cudaError_t e) {
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int kMaxSmemBytes = 232448;  // shared memory one CTA may ask for
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -183,20 +186,22 @@ smla_status launch_mma(const PartialParams &p, int grid, cudaStream_t st) {
 smla_status encode_cache_tiles(CUtensorMap *map, const void *cache, int64_t num_pages);
 namespace {
 
-template <bool DIRECT>
+template <bool DIRECT, bool Q4 = false>
 smla_status launch_tc(const PartialParams &p, int grid, cudaStream_t st) {
-    const void *fn = reinterpret_cast<const void *>(&smla::smla_partial_tc_kernel<DIRECT>);
-    cudaError_t e = ensure_smem_attr(fn, smla::TcCfg::kSmemBytes);
+    using C = smla::TcCfgT<Q4>;
+    const void *fn = reinterpret_cast<const void *>(&smla::smla_partial_tc_kernel<DIRECT, Q4>);
+    cudaError_t e = ensure_smem_attr(fn, C::kSmemBytes);
     if (e != cudaSuccess) return cuda_fail(e);
-    // dense lists load whole half-pages by TMA; sparse lists never use the map
+    // dense lists of bf16 rows load whole half-pages by TMA; sparse lists and
+    // 4-bit rows never use the map
     CUtensorMap map;
     std::memset(&map, 0, sizeof map);
-    if (p.seq_lens != nullptr && p.K > 0) {
+    if (!Q4 && p.seq_lens != nullptr && p.K > 0) {
         const smla_status s = encode_cache_tiles(&map, p.cache, p.num_pages);
         if (s != SMLA_OK) return s;
     }
-    e = launch_dependent(smla::smla_partial_tc_kernel<DIRECT>, grid, smla::TcCfg::kThreads,
-                         smla::TcCfg::kSmemBytes, st, p, map);
+    e = launch_dependent(smla::smla_partial_tc_kernel<DIRECT, Q4>, grid, C::kThreads, C::kSmemBytes, st,
+                         p, map);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
@@ -1146,6 +1151,327 @@ smla_status smla_indexer_topk(const void *q_index, const float *w, const void *k
                           max_n, plan, scores, max_n, sel_ws, s);
     if (st != SMLA_OK) return st;
     return launch_ix_select(scores, max_n, n_vis, B, T, max_n, K, sel_ws, topk_idx, true, s);
+}
+
+// ---------------------------------------------------------------------------
+// The 4-bit latent cache (see include/smla.h and smla_q4.cuh).
+}  // extern "C"
+
+namespace {
+
+// The page table of an entry point that walks it.
+smla_status check_pages(const void *cache, int64_t num_pages, const int32_t *page_table, int pt_stride,
+                        int page_size) {
+    if (page_size != SMLA_PAGE_SIZE) return SMLA_ERR_UNSUPPORTED;
+    if (cache == nullptr || page_table == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (num_pages < 1 || pt_stride < 1) return SMLA_ERR_INVALID_ARG;
+    if (num_pages > SMLA_MAX_PAGES) return SMLA_ERR_UNSUPPORTED;
+    if (!aligned(cache, 16) || !aligned(page_table, 4)) return SMLA_ERR_MISALIGNED;
+    return SMLA_OK;
+}
+
+// Partials of n slots of 512 + 2 floats inside a workspace.
+void set_partials(PartialParams *p, void *workspace, size_t n) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t off_m = round256(n * smla::kDc * sizeof(float));
+    const size_t off_l = off_m + round256(n * sizeof(float));
+    p->part_o = reinterpret_cast<float *>(ws);
+    p->part_m = reinterpret_cast<float *>(ws + off_m);
+    p->part_lse = reinterpret_cast<float *>(ws + off_l);
+}
+
+}  // namespace
+
+extern "C" {
+
+smla_status smla_q4_append(const void *rows, int n_rows, const int32_t *cu_rows, const int32_t *start,
+                           int B, void *cache_q4, int64_t num_pages, const int32_t *page_table,
+                           int pt_stride, int page_size, void *stream) {
+    if (n_rows < 0 || B < 0) return SMLA_ERR_INVALID_ARG;
+    if (n_rows == 0 || B == 0) return page_size == SMLA_PAGE_SIZE ? SMLA_OK : SMLA_ERR_UNSUPPORTED;
+    const smla_status st = check_pages(cache_q4, num_pages, page_table, pt_stride, page_size);
+    if (st != SMLA_OK) return st;
+    if (!rows || !cu_rows || !start) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(rows, 16) || !aligned(cu_rows, 4) || !aligned(start, 4)) return SMLA_ERR_MISALIGNED;
+    smla::Q4AppendParams p{};
+    p.rows = static_cast<const __nv_bfloat16 *>(rows);
+    p.n_rows = n_rows;
+    p.cu_rows = cu_rows;
+    p.start = start;
+    p.B = B;
+    p.page_table = page_table;
+    p.pt_stride = pt_stride;
+    p.num_pages = num_pages;
+    p.cache = static_cast<uint8_t *>(cache_q4);
+    const int grid = (int)(((long long)n_rows + smla::kQ4Warps - 1) / smla::kQ4Warps);
+    const cudaError_t e = launch_dependent(smla::smla_q4_append_kernel, grid, 32 * smla::kQ4Warps, 0,
+                                           static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+}
+
+smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t *page_table, int pt_stride,
+                         const int32_t *positions, int B, int K, int page_size, void *rows, void *stream) {
+    if (B < 0 || K < 0) return SMLA_ERR_INVALID_ARG;
+    if (B == 0 || K == 0) return page_size == SMLA_PAGE_SIZE ? SMLA_OK : SMLA_ERR_UNSUPPORTED;
+    const smla_status st = check_pages(cache_q4, num_pages, page_table, pt_stride, page_size);
+    if (st != SMLA_OK) return st;
+    if (!positions || !rows) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(positions, 4) || !aligned(rows, 16)) return SMLA_ERR_MISALIGNED;
+    const long long blocks = ((long long)B * K + smla::kQ4Warps - 1) / smla::kQ4Warps;
+    if (blocks > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    smla::Q4ReadParams p{};
+    p.cache = static_cast<const uint8_t *>(cache_q4);
+    p.num_pages = num_pages;
+    p.page_table = page_table;
+    p.pt_stride = pt_stride;
+    p.positions = positions;
+    p.B = B;
+    p.K = K;
+    p.out = static_cast<__nv_bfloat16 *>(rows);
+    const cudaError_t e = launch_dependent(smla::smla_q4_read_kernel, (int)blocks, 32 * smla::kQ4Warps, 0,
+                                           static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+}
+
+int smla_q4_nsplit(int B, int T, int H, int K) {
+    if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
+    return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
+}
+
+smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                           const int32_t *page_table, int pt_stride, const int32_t *topk_idx, int B,
+                           int T, int H, int K, int page_size, float scale, int nsplit, void *workspace,
+                           size_t workspace_bytes, void *o, float *lse, void *stream) {
+    smla_status st = check_decode_args(q, cache_q4, num_pages, page_table, pt_stride, topk_idx, B, T, H, K,
+                                       page_size, scale);
+    if (st != SMLA_OK) return st;
+    if (nsplit < 0 || nsplit > SMLA_MAX_NSPLIT || K > SMLA_MAX_K) return SMLA_ERR_INVALID_ARG;
+    if (B == 0 || T == 0 || H == 0) return SMLA_OK;
+    if (o == nullptr || lse == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(lse, 4)) return SMLA_ERR_MISALIGNED;
+    if (nsplit == 0) nsplit = smla_q4_nsplit(B, T, H, K);
+    const long long grid = (long long)B * T * nsplit;
+    if (grid > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PartialParams p = make_params(q, cache_q4, num_pages, page_table, pt_stride, topk_idx, B, T, H, K, scale,
+                                  nsplit);
+    if (nsplit == 1) {
+        p.o = static_cast<__nv_bfloat16 *>(o);
+        p.lse = lse;
+        return launch_tc<true, true>(p, (int)grid, s);
+    }
+    if (workspace_bytes < smla_workspace_bytes(B, T, H, nsplit)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
+    set_partials(&p, workspace, (size_t)B * T * H * nsplit);
+    st = launch_tc<false, true>(p, (int)grid, s);
+    if (st != SMLA_OK) return st;
+    return launch_combine(p.part_o, p.part_m, p.part_lse, B, T, H, nsplit, o, lse, s);
+}
+
+int smla_dense_q4_nsplit(int B, int T, int H, int K) { return smla_dense_nsplit(B, T, H, K); }
+
+size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {
+    return smla_dense_workspace_bytes(B, T, H, K, nsplit);
+}
+
+smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                                 const int32_t *page_table, int pt_stride, const int32_t *seq_lens, int B,
+                                 int T, int H, int K, int page_size, float scale, int nsplit,
+                                 void *workspace, size_t workspace_bytes, void *o, float *lse,
+                                 void *stream) {
+    smla_status st = check_dense_args(q, cache_q4, num_pages, page_table, pt_stride, seq_lens, B, T, H, K,
+                                      page_size, scale, nsplit);
+    if (st != SMLA_OK) return st;
+    if (K > SMLA_MAX_K) return SMLA_ERR_INVALID_ARG;
+    if (B == 0 || T == 0 || H == 0) return SMLA_OK;
+    if (o == nullptr || lse == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(lse, 4)) return SMLA_ERR_MISALIGNED;
+    DensePlan d = dense_plan(B, T, H, K, nsplit);
+    const int kc64 = K > 0 ? ((K + d.nsplit - 1) / d.nsplit + 63) / 64 * 64 : 0;
+    if (K > 0) d.nsplit = (K + kc64 - 1) / kc64;
+    if ((long long)B * d.units * d.nsplit > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PartialParams p = dense_params(q, cache_q4, num_pages, page_table, pt_stride, seq_lens, B, T, H, K,
+                                   scale, d);
+    if (K > 0) p.kc = kc64;
+    const int grid = B * d.units * d.nsplit;
+    if (d.nsplit == 1) {
+        p.o = static_cast<__nv_bfloat16 *>(o);
+        p.lse = lse;
+        return launch_tc<true, true>(p, grid, s);
+    }
+    if (workspace_bytes < smla_workspace_bytes(B, T, H, d.nsplit)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
+    set_partials(&p, workspace, (size_t)B * T * H * d.nsplit);
+    st = launch_tc<false, true>(p, grid, s);
+    if (st != SMLA_OK) return st;
+    return launch_combine(p.part_o, p.part_m, p.part_lse, B, T, H, d.nsplit, o, lse, s);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Eviction by accumulated attention weight (see include/smla.h and
+// smla_evict.cuh).
+static_assert(smla::plan_fixed_bytes(SMLA_EVICT_MAX_N) <= kMaxSmemBytes, "eviction bitmaps must fit shared memory");
+static_assert(smla::kEvictBuffers == SMLA_EVICT_MAX_CACHES, "caches per apply call");
+
+namespace {
+
+template <bool Q4, int HG>
+cudaError_t launch_weigh_rows(const smla::WeighParams &p, int grid, cudaStream_t st) {
+    using C = smla::WeighCfg<HG>;
+    const cudaError_t e = ensure_smem_attr(
+        reinterpret_cast<const void *>(&smla::smla_evict_weigh_kernel<Q4, HG>), C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(smla::smla_evict_weigh_kernel<Q4, HG>, grid, 32 * smla::kWeighWarps,
+                            C::kSmemBytes, st, p);
+}
+
+template <bool Q4>
+smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages, const int32_t *page_table,
+                             int pt_stride, const int32_t *seq_lens, const float *lse, int B, int T, int H,
+                             int page_size, float scale, float *acc, int max_n, void *stream) {
+    if (B < 0 || T < 0 || H < 0 || max_n < 0 || !std::isfinite(scale)) return SMLA_ERR_INVALID_ARG;
+    if (page_size != SMLA_PAGE_SIZE || H > SMLA_MAX_HEADS) return SMLA_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0 || H == 0 || max_n == 0) return SMLA_OK;
+    if (max_n > SMLA_MAX_K || (long long)B * T * H > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    const smla_status s = check_pages(cache, num_pages, page_table, pt_stride, page_size);
+    if (s != SMLA_OK) return s;
+    if (!q || !seq_lens || !lse || !acc) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(acc, 4))
+        return SMLA_ERR_MISALIGNED;
+    smla::WeighParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.num_pages = num_pages;
+    p.page_table = page_table;
+    p.pt_stride = pt_stride;
+    p.seq_lens = seq_lens;
+    p.lse = lse;
+    p.B = B;
+    p.T = T;
+    p.H = H;
+    p.scale_log2 = scale * smla::kLog2e;
+    p.acc = acc;
+    p.max_n = max_n;
+    const long long tiles = ((long long)max_n + smla::kWeighTile - 1) / smla::kWeighTile;
+    const long long most = (tiles + smla::kWeighWarps - 1) / smla::kWeighWarps;
+    p.nchunk = (int)std::max<long long>(1, std::min<long long>(most, (2ll * current_device_sms() + B - 1) / B));
+    if ((long long)B * p.nchunk > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    const int grid = B * p.nchunk;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long rows = (long long)T * H;
+    const cudaError_t e = rows <= 16   ? launch_weigh_rows<Q4, 1>(p, grid, st)
+                          : rows <= 32 ? launch_weigh_rows<Q4, 2>(p, grid, st)
+                                       : launch_weigh_rows<Q4, 4>(p, grid, st);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+smla_status smla_evict_accumulate(const void *q, const void *kv_cache, int64_t num_pages,
+                                  const int32_t *page_table, int pt_stride, const int32_t *seq_lens,
+                                  const float *lse, int B, int T, int H, int page_size, float scale,
+                                  float *acc, int max_n, void *stream) {
+    return evict_accumulate<false>(q, kv_cache, num_pages, page_table, pt_stride, seq_lens, lse, B, T, H,
+                                   page_size, scale, acc, max_n, stream);
+}
+
+smla_status smla_evict_accumulate_q4(const void *q, const void *cache_q4, int64_t num_pages,
+                                     const int32_t *page_table, int pt_stride, const int32_t *seq_lens,
+                                     const float *lse, int B, int T, int H, int page_size, float scale,
+                                     float *acc, int max_n, void *stream) {
+    return evict_accumulate<true>(q, cache_q4, num_pages, page_table, pt_stride, seq_lens, lse, B, T, H,
+                                  page_size, scale, acc, max_n, stream);
+}
+
+size_t smla_evict_workspace_bytes(int B, int max_n) {
+    if (B < 0 || max_n < 0) return 0;
+    return round256((size_t)B * max_n * sizeof(int));
+}
+
+smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t *n, int B, int max_n, int K,
+                            int n_sink, int n_recent, void *workspace, size_t workspace_bytes,
+                            int32_t *src, int32_t *n_new, float *acc_new, int32_t *pos_new, void *stream) {
+    if (B < 0 || max_n < 0 || K < 1 || n_sink < 0 || n_recent < 0) return SMLA_ERR_INVALID_ARG;
+    if ((long long)n_sink + n_recent > K) return SMLA_ERR_INVALID_ARG;
+    if (max_n > SMLA_EVICT_MAX_N || K > SMLA_MAX_K) return SMLA_ERR_UNSUPPORTED;
+    if (B == 0) return SMLA_OK;
+    if (!n || !src || !n_new || (max_n > 0 && !acc)) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(acc, 4) || !aligned(pos, 4) || !aligned(n, 4) || !aligned(src, 4) || !aligned(n_new, 4) ||
+        !aligned(acc_new, 4) || !aligned(pos_new, 4))
+        return SMLA_ERR_MISALIGNED;
+    const size_t cells = (size_t)B * max_n * 4;
+    if (overlap(acc, cells, acc_new, cells) || overlap(pos, cells, pos_new, cells) ||
+        overlap(n, (size_t)B * 4, n_new, (size_t)B * 4))
+        return SMLA_ERR_INVALID_ARG;
+    if (workspace_bytes < smla_evict_workspace_bytes(B, max_n)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    if (max_n > 0 && workspace == nullptr) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
+    smla::EvictPlanParams p{};
+    p.acc = acc;
+    p.pos = pos;
+    p.n = n;
+    p.B = B;
+    p.max_n = max_n;
+    p.K = K;
+    p.n_sink = n_sink;
+    p.n_recent = n_recent;
+    p.movers = static_cast<int *>(workspace);
+    p.src = src;
+    p.n_new = n_new;
+    p.acc_new = acc_new;
+    p.pos_new = pos_new;
+    int smem = smla::plan_fixed_bytes(max_n);
+    p.cached = smem + 4ll * max_n <= kMaxSmemBytes;
+    if (p.cached) smem += 4 * max_n;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_evict_plan_kernel), kMaxSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = launch_dependent(smla::smla_evict_plan_kernel, B, smla::kPlanThreads, (size_t)smem,
+                         static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+}
+
+smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *page_table, int pt_stride,
+                             int64_t num_pages, int page_size, void *const *caches, const int32_t *row_bytes,
+                             int n_caches, void *stream) {
+    if (B < 0 || K < 0 || n_caches < 0) return SMLA_ERR_INVALID_ARG;
+    if (n_caches > SMLA_EVICT_MAX_CACHES || page_size != SMLA_PAGE_SIZE) return SMLA_ERR_UNSUPPORTED;
+    if (B == 0 || K == 0 || n_caches == 0) return SMLA_OK;
+    if (!src || !caches || !row_bytes) return SMLA_ERR_INVALID_ARG;
+    if (!aligned(src, 4)) return SMLA_ERR_MISALIGNED;
+    smla::EvictApplyParams p{};
+    for (int k = 0; k < n_caches; ++k) {
+        const smla_status st = check_pages(caches[k], num_pages, page_table, pt_stride, page_size);
+        if (st != SMLA_OK) return st;
+        if (row_bytes[k] < 1 || row_bytes[k] > SMLA_EVICT_MAX_ROW_BYTES) return SMLA_ERR_UNSUPPORTED;
+        if (row_bytes[k] % 16) return SMLA_ERR_MISALIGNED;
+        p.buf[k] = static_cast<uint8_t *>(caches[k]);
+        p.row_bytes[k] = row_bytes[k];
+    }
+    p.src = src;
+    p.B = B;
+    p.K = K;
+    p.page_table = page_table;
+    p.pt_stride = pt_stride;
+    p.num_pages = num_pages;
+    p.n_buf = n_caches;
+    const long long units = (long long)B * ((K + 31ll) / 32);
+    const long long blocks = (units + smla::kApplyWarps - 1) / smla::kApplyWarps;
+    if (blocks > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    const cudaError_t e = launch_dependent(smla::smla_evict_apply_kernel, (int)blocks, 32 * smla::kApplyWarps, 0,
+                                           static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
 }  // extern "C"

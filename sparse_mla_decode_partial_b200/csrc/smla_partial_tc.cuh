@@ -62,17 +62,22 @@
 #include <cuda_bf16.h>
 
 #include "smla_partial_mma.cuh"
+#include "smla_q4.cuh"
 #include "smla_tc_ptx.cuh"
 
 namespace smla {
 
 constexpr int kMaxTcRows = 64;  // query rows (the MMA's M) of one CTA
 
-struct TcCfg {
 #ifndef SMLA_TC_PRODUCER_WARPS
 #define SMLA_TC_PRODUCER_WARPS 11
 #endif
-    static constexpr int kProducerWarps = SMLA_TC_PRODUCER_WARPS;
+// Q4: the cache holds 4-bit rows.  Twelve producer warps then decode: a tile
+// is 512 (row, group) units and 256 16-byte pieces of rope values, two units
+// per producer thread.
+template <bool Q4>
+struct TcCfgT {
+    static constexpr int kProducerWarps = Q4 ? 12 : SMLA_TC_PRODUCER_WARPS;
     static constexpr int kMmaWarp = 4 + kProducerWarps;
     static constexpr int kThreads = 32 * (kMmaWarp + 1);
     static constexpr int kTileRows = 32;
@@ -102,12 +107,25 @@ struct TcCfg {
     }
     static constexpr float kTau = 8.0f;                     // lazy-rescale threshold (log2 units)
 };
+using TcCfg = TcCfgT<false>;
 static_assert(TcCfg::kSmemBytes <= 232448, "shared memory per CTA");
+static_assert(32 * TcCfgT<true>::kProducerWarps * 2 == 32 * kQ4Groups + 32 * 8, "two units per producer thread");
 
-template <bool DIRECT>
-__global__ void __launch_bounds__(TcCfg::kThreads, 1)
+// What one producer thread holds of a tile of 4-bit rows: two of its 768
+// units.  Unit u < 512 is group (u / 8) % 16 of row u % 8 + 8 (u / 128): eight
+// lanes write the same group of eight rows, whose swizzled 16-byte chunks fall
+// in distinct banks, and a warp reads 64 bytes of each row.  The others are
+// 16-byte pieces of rope values, v = u - 512: piece (v / 8) % 8 of row v % 8 +
+// 8 (v / 64).
+struct Q4Units {
+    uint4 d[2];
+    uint32_t s2[2];  // the group's scale, twice
+};
+
+template <bool DIRECT, bool Q4 = false>
+__global__ void __launch_bounds__(TcCfgT<Q4>::kThreads, 1)
     smla_partial_tc_kernel(const PartialParams p, const __grid_constant__ CUtensorMap map_kv) {
-    using C = TcCfg;
+    using C = TcCfgT<Q4>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // 1024-byte aligned base (128B-swizzle atoms are 8 rows x 128 B).
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -151,7 +169,8 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         for (int i = 0; i < C::kStages; ++i) {
             // 32 cp.async arrivals per producer warp + one plain arrive that
             // publishes the tile's validity mask
-            mbar_init(&kv_full[i], 32 * C::kProducerWarps + 1);
+            // (Q4: one plain arrival per producer warp instead)
+            mbar_init(&kv_full[i], (Q4 ? 1 : 32) * C::kProducerWarps + 1);
             mbar_init(&kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -253,6 +272,71 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
             }
             named_bar_sync(bar_prod, 32 * C::kProducerWarps);  // rows_s complete
             const int chunk_tiles = (n + C::kTileRows - 1) / C::kTileRows;
+            if constexpr (Q4) {
+                // Two units per thread and tile; the next tile's loads are in
+                // flight while this one is decoded.
+                auto unit_row = [&](int t, int u) {
+                    const int r = u < 512 ? (u & 7) + 8 * (u >> 7) : (u & 7) + 8 * ((u - 512) >> 6);
+                    const int j = t * C::kTileRows + r;
+                    return j < n ? rows_s[j] : -1;
+                };
+                auto load = [&](int t, Q4Units &x) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int u = ptid + k * kPT;
+                        const int row = unit_row(t, u);
+                        x.d[k] = make_uint4(0u, 0u, 0u, 0u);
+                        x.s2[k] = 0u;  // a padding slot decodes to zeros
+                        if (row < 0) continue;
+                        const uint8_t *src = cache + (size_t)row * kQ4RowBytes;
+                        if (u < 512) {
+                            const int g = (u >> 3) & 15;
+                            x.d[k] = ld_row16(src + 16 * g);
+                            x.s2[k] = ld_scale2(src + kQ4OffScale + 2 * g);
+                        } else {
+                            x.d[k] = ld_row16(src + kQ4OffRope + 16 * ((u >> 3) & 7));
+                        }
+                    }
+                };
+                Q4Units cur, next;
+                load(0, cur);
+                for (int t = 0; t < chunk_tiles; ++t, ++it) {
+                    const int stage = it % C::kStages;
+                    if (t + 1 < chunk_tiles) load(t + 1, next);
+                    if (it >= C::kStages) mbar_wait(&kv_empty[stage], ((it / C::kStages) - 1) & 1, dead);
+                    uint8_t *dst = smem + C::kOffKV + C::tile_off(stage);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int u = ptid + k * kPT;
+                        if (u < 512) {
+                            const int r = (u & 7) + 8 * (u >> 7), g = (u >> 3) & 15;
+                            uint8_t *line = dst + (g >> 1) * C::kBoxStride + r * 128;
+                            const uint32_t bias = q4_bias(cur.s2[k]);
+                            const uint32_t w[4] = {cur.d[k].x, cur.d[k].y, cur.d[k].z, cur.d[k].w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4 *>(line + (((4 * (g & 1) + i) ^ (r & 7)) << 4)) =
+                                    q4_word(w[i], cur.s2[k], bias);
+                        } else {
+                            const int r = (u & 7) + 8 * ((u - 512) >> 6), ch = (u >> 3) & 7;
+                            *reinterpret_cast<uint4 *>(dst + 8 * C::kBoxStride + r * 128 +
+                                                       ((ch ^ (r & 7)) << 4)) = cur.d[k];
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (pw == 0) {
+                        const int j = t * C::kTileRows + lane;
+                        const uint32_t vmask = __ballot_sync(0xffffffffu, j < n && rows_s[j] >= 0);
+                        if (lane == 0) {
+                            hdr[stage] = vmask;
+                            mbar_arrive(&kv_full[stage]);
+                        }
+                    }
+                    if (lane == 0) mbar_arrive(&kv_full[stage]);
+                    cur = next;
+                }
+            } else
             for (int t = 0; t < chunk_tiles; ++t, ++it) {
                 const int stage = it % C::kStages;
                 if (it >= C::kStages) mbar_wait(&kv_empty[stage], ((it / C::kStages) - 1) & 1, dead);
@@ -538,6 +622,9 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
 
         // ---- epilogue: O (unnormalised) and m, lse of head hrow
         const float l_tot = l_acc + __shfl_xor_sync(0xffffffffu, l_acc, 16);
+        // whether anything was attended to; 4-bit rows: a NaN score (a row that
+        // held no finite value) counts, and makes o and lse NaN
+        const bool some = Q4 ? !(l_tot == 0.f) : l_tot > 0.f;
         if (n_pairs > 0) {
             mbar_wait(&o_done[(n_pairs - 1) & 1], ((n_pairs - 1) >> 1) & 1, dead);
             tc_fence_after();
@@ -584,7 +671,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
                 }
                 __syncwarp();
             } else if (write) {
-                const float inv = (l_tot > 0.f) ? 1.f / l_tot : 0.f;
+                const float inv = some ? 1.f / l_tot : 0.f;
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * kDc + col);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -596,10 +683,12 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
             }
         }
         if (write && half == 0) {
-            const float lse_v = (l_tot > 0.f) ? (m_ref + log2f(l_tot)) * kLn2 : -INFINITY;
+            const float lse_v = some ? (m_ref + log2f(l_tot)) * kLn2 : -INFINITY;
             if (!DIRECT) {
                 const size_t k = row * p.nsplit + s;
-                p.part_m[k] = (l_tot > 0.f) ? m_ref * kLn2 : -INFINITY;
+                // (a NaN sum whose every score was NaN keeps a finite reference,
+                // so that the combine does not take the split for an empty one)
+                p.part_m[k] = some ? (Q4 && m_ref == -INFINITY ? 0.f : m_ref * kLn2) : -INFINITY;
                 p.part_lse[k] = lse_v;
             } else {
                 p.lse[row] = lse_v;

@@ -1,0 +1,283 @@
+"""Eviction on the GPU: accumulated weights, plans, moves, and a run of the
+whole cache's life, against plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_util as cu
+from sparse_mla_decode_partial_b200 import binding
+from test_gpu_q4 import SCALE, clean_device, fill  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+
+
+def make_cache(paged, q4, seed):
+    if q4:
+        return fill(paged, None, seed)
+    rows = cu.latents(paged.pages * 64, seed)
+    return rows.view(paged.pages, 64, 576).cuda(), cu.f64(rows)
+
+
+def check_weights(acc, before, q, lse, lens, rows_of, what):
+    """acc against the definition.  A weight exp(x) with x off by dx (the score's
+    bound of cache_util.attend and 2^-22 of |x| + |lse|, both parts of lse
+    exact to 2^-48) is off by 2 dx of itself, ex2 adds 2^-21; the row sums and
+    the addition to acc round once per term."""
+    want, tol = before.copy(), np.zeros_like(before)
+    B, T, H = lse.shape
+    for b in range(B):
+        for t in range(T):
+            n = int(lens[b, t])
+            if n == 0:
+                continue
+            kv = rows_of(b, n)
+            s = q[b, t] @ kv.T * SCALE
+            ds = 580 * 2.0 ** -23 * SCALE * (np.abs(q[b, t]) @ np.abs(kv).T) + 2.0 ** -22 * (np.abs(s) + np.abs(lse[b, t])[:, None] + 1)
+            live = np.isfinite(lse[b, t])
+            w = np.exp(s[live] - lse[b, t][live][:, None])
+            want[b, :n] += w.sum(0)
+            tol[b, :n] += (w * (2 * ds[live] + 2.0 ** -20 + 2.0 ** -23 * T * H)).sum(0)
+    cu.check(acc, want, tol + 2.0 ** -23 * np.abs(want) + 1e-37, what)
+
+
+def run_weigh(lens, H, q4, seed=0, max_n=None, lse_edit=None):
+    lens = np.asarray(lens, np.int32)
+    B, T = lens.shape
+    most = int(lens.max()) if max_n is None else max_n
+    paged = cu.Paged([max(int(x.max()), 1) for x in lens], seed)
+    cache, vals = make_cache(paged, q4, seed + 1)
+    q = cu.queries(B, T, H, seed + 2)
+    qd = cu.f64(q)
+    lse = np.full((B, T, H), -INF)
+    for b in range(B):
+        for t in range(T):
+            if lens[b, t]:
+                lse[b, t] = cu.attend(qd[b, t], vals[paged.rows(b, range(lens[b, t]))], SCALE)[1]
+    if lse_edit:
+        lse_edit(lse)
+    lse32 = torch.from_numpy(lse).float()
+    acc = torch.rand(B, most, generator=torch.Generator().manual_seed(seed)) * 0.01
+    got = acc.cuda()
+    out = binding.evict_accumulate(q.cuda(), cache, paged.cuda, torch.from_numpy(lens).cuda(), lse32.cuda(), SCALE, got)
+    assert out is got
+    check_weights(got, acc.double().numpy(), qd, lse32.double().numpy(), lens,
+                  lambda b, n: vals[paged.rows(b, range(n))], f"lens {lens.tolist()} H {H} q4 {q4}")
+    again = acc.cuda()
+    binding.evict_accumulate(q.cuda(), cache, paged.cuda, torch.from_numpy(lens).cuda(), lse32.cuda(), SCALE, again)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 16), (1, 17), (2, 16), (3, 8), (9, 8), (1, 64), (5, 64), (2, 40)])
+def test_weights_over_query_rows(T, H, q4):
+    run_weigh([[200 + t for t in range(T)], [31 + t for t in range(T)]], H, q4, seed=T + H)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("lens", [[[0]], [[1]], [[0], [5], [0]], [[31], [32], [33]], [[64], [65], [1500]], [[0, 70, 3, 64]]])
+def test_weights_over_lengths(lens, q4):
+    run_weigh(lens, 16, q4, seed=len(lens), max_n=1600)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_weights_of_rows_with_empty_and_infinite_lse(q4):
+    def edit(lse):
+        lse[0, 0, 3] = -INF
+        lse[0, 1, 2] = INF
+    run_weigh([[90, 100]], 8, q4, lse_edit=edit)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_weights_ignore_what_lies_behind_the_length(q4):
+    """NaN rows in the masked part of a page and of the pool change nothing."""
+    paged = cu.Paged([40], 1)
+    cache, vals = make_cache(paged, q4, 2)
+    q, lens = cu.queries(1, 2, 16, 3), torch.tensor([[30, 37]], dtype=torch.int32).cuda()
+    lse = torch.zeros(1, 2, 16).cuda() + 4.0
+    acc = torch.zeros(1, 40).cuda()
+    binding.evict_accumulate(q.cuda(), cache, paged.cuda, lens, lse, SCALE, acc)
+    flat = cache.view(-1, cache.shape[-1])
+    keep = set(paged.rows(0, range(37)).tolist())
+    dead = torch.tensor([r for r in range(flat.shape[0]) if r not in keep]).cuda()
+    flat[dead] = 0xFF if q4 else float("nan")
+    acc2 = torch.zeros(1, 40).cuda()
+    binding.evict_accumulate(q.cuda(), cache, paged.cuda, lens, lse, SCALE, acc2)
+    assert torch.equal(acc, acc2) and not acc[0, 37:].any()
+
+
+def test_weights_count_bad_lengths_and_pages():
+    paged = cu.Paged([128, 128], 1)
+    paged.table[0, 1] = 10 ** 6
+    cache, vals = make_cache(paged, False, 2)
+    q, lse = cu.queries(2, 1, 4, 3).cuda(), torch.zeros(2, 1, 4).cuda()
+    acc = torch.zeros(2, 100).cuda()
+    lens = torch.tensor([[100], [-3]], dtype=torch.int32).cuda()
+    binding.evict_accumulate(q, cache, paged.cuda, lens, lse, SCALE, acc)
+    assert binding.check_device(clear=True) == (5, 36 + 1)
+    assert acc[0, :64].all() and not acc[0, 64:].any() and not acc[1].any()
+
+
+# ---------------------------------------------------------------- plan
+def run_plan(acc, n, K, pos=None, n_sink=0, n_recent=0):
+    B, most = acc.shape
+    p = binding.evict_plan(torch.from_numpy(acc).float().cuda(), torch.tensor(n, dtype=torch.int32).cuda(), K,
+                           pos=None if pos is None else torch.from_numpy(pos).cuda(), n_sink=n_sink, n_recent=n_recent)
+    src = np.full((B, K), -1, np.int32)
+    a_new, p_new = np.zeros((B, most), np.float32), np.full((B, most), -1, np.int32)
+    for b in range(B):
+        ps = np.arange(most, dtype=np.int32) if pos is None else pos[b]
+        s = cu.plan(acc[b].astype(np.float32).tolist(), ps.tolist(), n[b], K, n_sink, n_recent)
+        src[b, :len(s)] = s
+        a_new[b, :len(s)], p_new[b, :len(s)] = acc[b].astype(np.float32)[s], ps[s]
+    np.testing.assert_array_equal(p.src.cpu().numpy(), src)
+    np.testing.assert_array_equal(p.n.cpu().numpy(), np.minimum(n, K))
+    np.testing.assert_array_equal(p.acc.cpu().numpy(), a_new)
+    np.testing.assert_array_equal(p.pos.cpu().numpy(), p_new)
+
+
+@pytest.mark.parametrize("most,n,K", [
+    (1, [1], 1), (1, [0], 1), (5, [5, 4, 0, 1], 3), (64, [64, 33], 32), (100, [100, 99, 65], 64), (100, [100], 200),
+    (1000, [1000, 1, 777], 1), (1000, [1000, 999], 998), (4097, [4097, 2048], 2048), (70001, [70001, 60000], 50000),
+])
+def test_plan_sizes(most, n, K):
+    rng = np.random.default_rng(most + K)
+    run_plan(rng.exponential(1.0, (len(n), most)), n, K)
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "zeros", "negative", "special"])
+def test_plan_ties_and_special_weights(kind):
+    rng = np.random.default_rng(1)
+    acc = rng.exponential(1.0, (3, 500))
+    if kind == "equal":
+        acc[:] = 0.25
+    elif kind == "few":
+        acc = np.round(acc)
+    elif kind == "zeros":
+        acc = np.where(acc < 1, -0.0, np.where(acc < 2, 0.0, acc))
+    elif kind == "negative":
+        acc = 1 - acc
+    else:
+        acc[:, ::7], acc[:, 1::7], acc[:, 2::7], acc[:, 3::7] = np.nan, INF, -INF, 1e-45
+    run_plan(acc, [500, 321, 40], 200)
+    run_plan(acc, [500, 321, 40], 33, n_sink=4, n_recent=20)
+
+
+@pytest.mark.parametrize("n_sink,n_recent", [(0, 0), (4, 0), (0, 30), (4, 30), (40, 60)])
+def test_plan_keeps_sinks_and_recent_positions(n_sink, n_recent):
+    rng = np.random.default_rng(2)
+    B, most = 3, 400
+    acc = rng.exponential(1.0, (B, most))
+    pos = np.stack([rng.permutation(most * 3)[:most] for _ in range(B)]).astype(np.int32)
+    run_plan(acc, [400, 399, 130], 100, pos=pos, n_sink=n_sink, n_recent=n_recent)
+    run_plan(acc, [400, 399, 130], 100, n_sink=n_sink, n_recent=n_recent)
+
+
+def test_plan_far_positions():
+    acc = np.arange(40, dtype=np.float64)[None]
+    pos = (np.arange(40)[None] + 2 ** 31 - 40).astype(np.int32)
+    run_plan(acc, [40], 10, pos=pos, n_sink=2, n_recent=3)
+
+
+def test_plan_clamps_and_counts_lengths():
+    acc = torch.rand(2, 10).cuda()
+    p = binding.evict_plan(acc, torch.tensor([-1, 11], dtype=torch.int32).cuda(), 20)
+    assert binding.check_device(clear=True) == (5, 2)
+    assert p.n.tolist() == [0, 10]
+
+
+# ---------------------------------------------------------------- apply
+@pytest.mark.parametrize("n,K", [([130, 64, 3], 50), ([700], 640), ([65, 66], 64)])
+def test_apply_moves_rows_of_every_buffer(n, K):
+    rng = np.random.default_rng(K)
+    paged = cu.Paged(n, 3)
+    bufs = [torch.randint(0, 256, (paged.pages, 64, w), dtype=torch.uint8, generator=torch.Generator().manual_seed(w)).cuda()
+            for w in (1152, 416, 256, 16)]
+    bufs[0] = bufs[0].view(torch.bfloat16)
+    acc = torch.from_numpy(rng.exponential(1.0, (len(n), max(n)))).float().cuda()
+    p = binding.evict_plan(acc, torch.tensor(n, dtype=torch.int32).cuda(), K)
+    before = [b.view(torch.uint8).cpu().numpy().reshape(paged.pages * 64, -1).copy() for b in bufs]
+    for _ in range(2):  # the second time changes nothing
+        binding.evict_apply(p.src, paged.cuda, bufs)
+        src = p.src.cpu().numpy()
+        for buf, old in zip(bufs, before):
+            want = old.copy()
+            for b in range(len(n)):
+                for i in range(min(n[b], K)):
+                    want[paged.row(b, i)] = old[paged.row(b, src[b, i])]
+            np.testing.assert_array_equal(buf.view(torch.uint8).cpu().numpy().reshape(paged.pages * 64, -1), want)
+
+
+def test_apply_leaves_out_and_counts_unmapped_rows():
+    paged = cu.Paged([128], 3)
+    buf = torch.randint(0, 256, (paged.pages, 64, 32), dtype=torch.uint8).cuda()
+    old = buf.cpu().numpy().reshape(-1, 32).copy()
+    src = torch.tensor([[0, 127, 500, -2, 4, -1]], dtype=torch.int32).cuda()
+    binding.evict_apply(src, paged.cuda, (buf,))
+    assert binding.check_device(clear=True) == (5, 2)
+    want = old.copy()
+    want[paged.row(0, 1)] = old[paged.row(0, 127)]
+    np.testing.assert_array_equal(buf.cpu().numpy().reshape(-1, 32), want)
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("q4", [False, True])
+def test_a_cache_lives_through_steps_and_evictions(q4):
+    """Rows enter, tokens decode over all of them, their weights accumulate, the
+    cache is cut back to its budget, and the next step decodes over what is
+    left: every step against 64 bits, on one stream without a synchronisation."""
+    B, H, budget, room = 3, 8, 96, 256
+    paged = cu.Paged([room] * B, 7)
+    table = paged.cuda
+    rng = np.random.default_rng(0)
+    cache = (torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8) if q4 else
+             torch.zeros(paged.pages, 64, 576, dtype=torch.bfloat16)).cuda()
+    held = [[] for _ in range(B)]                 # (position, values) by slot
+    acc = torch.zeros(B, room).cuda()
+    pos = torch.full((B, room), -1, dtype=torch.int32).cuda()
+    n = torch.zeros(B, dtype=torch.int32).cuda()
+    nxt = [0] * B
+    for step in range(4):
+        new = [int(rng.integers(40, 90)) for _ in range(B)]
+        rows = cu.latents(sum(new), 100 + step)
+        at, cnt = 0, [len(h) for h in held]
+        stored = cu.values(cu.quantise(rows)) if q4 else cu.f64(rows)
+        offs = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+        if q4:
+            binding.q4_append(rows.cuda(), cache, table, offs, n)
+        for b in range(B):
+            if not q4:
+                flat = cache.view(-1, 576)
+                flat[torch.from_numpy(paged.rows(b, range(cnt[b], cnt[b] + new[b]))).cuda()] = rows[at:at + new[b]].cuda()
+            pos[b, cnt[b]:cnt[b] + new[b]] = torch.arange(nxt[b], nxt[b] + new[b]).int().cuda()
+            held[b] += [(nxt[b] + k, stored[at + k]) for k in range(new[b])]
+            nxt[b] += new[b]
+            at += new[b]
+        n = n + torch.tensor(new, dtype=torch.int32).cuda()
+        q = cu.queries(B, 1, H, 200 + step)
+        lens = n[:, None].contiguous()
+        most = max(len(h) for h in held)
+        decode = binding.decode_dense_q4 if q4 else binding.decode_dense
+        o, lse = decode(q.cuda(), cache, table, lens, SCALE, K=most)
+        before = acc.double().cpu().numpy()
+        binding.evict_accumulate(q.cuda(), cache, table, lens, lse, SCALE, acc)
+        p = binding.evict_plan(acc, n, budget, pos=pos, n_sink=4, n_recent=32)
+        vals = [np.stack([v for _, v in h]) for h in held]
+        if q4:
+            cu.check_attention(o, lse, q, lambda b, t: vals[b], SCALE, f"step {step}")
+        check_weights(acc, before, cu.f64(q), lse.double().cpu().numpy(), lens.cpu().numpy(),
+                      lambda b, k: vals[b][:k], f"step {step}")
+        for b in range(B):
+            s = cu.plan(acc[b].cpu().tolist(), pos[b].tolist(), len(held[b]), budget, 4, 32)
+            np.testing.assert_array_equal(p.src[b, :len(s)].cpu().numpy(), s)
+            held[b] = [held[b][i] for i in s]
+            assert p.pos[b, :len(s)].tolist() == [h[0] for h in held[b]]
+        binding.evict_apply(p.src, table, (cache,))
+        acc, pos, n = p.acc, p.pos, p.n
+    raw = cache.cpu()
+    for b in range(B):
+        at = paged.rows(b, range(len(held[b])))
+        got = cu.values(raw.numpy().reshape(-1, cu.ROW)[at]) if q4 else cu.f64(raw.view(-1, 576)[at])
+        np.testing.assert_array_equal(got, np.stack([v for _, v in held[b]]))

@@ -1,0 +1,364 @@
+"""The 4-bit latent cache on the GPU: quantise-and-append, read back, sparse and
+dense decode, against plain 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import cache_util as cu
+from sparse_mla_decode_partial_b200 import binding
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / 24.0
+
+
+@pytest.fixture(autouse=True)
+def clean_device():
+    binding.check_device(clear=True)
+    yield
+    assert binding.check_device(clear=True) == (0, 0)
+
+
+def fill(paged, lens, seed, std=0.7):
+    """A 4-bit cache of random rows (every row of the pool), as bytes on both sides."""
+    rows = cu.latents(paged.pages * 64, seed, std)
+    table = torch.arange(paged.pages, dtype=torch.int32)[None].cuda()
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    n = rows.shape[0]
+    binding.q4_append(rows.cuda(), cache, table, torch.tensor([0, n], dtype=torch.int32).cuda(),
+                      torch.zeros(1, dtype=torch.int32).cuda())
+    return cache, cu.values(cache.cpu().numpy().reshape(n, cu.ROW))
+
+
+# ---------------------------------------------------------------- append, read
+@pytest.mark.parametrize("new,start", [
+    ([0], [0]), ([1], [0]), ([1], [63]), ([65], [1]), ([3, 0, 70, 1], [60, 5, 0, 127]), ([0, 0, 2], [1, 2, 3]),
+    ([1] * 17, list(range(17))), ([200, 1, 33], [0, 64, 95]),
+])
+def test_append_writes_the_definition(new, start):
+    paged = cu.Paged([a + n for a, n in zip(start, new)], seed=len(new))
+    n = sum(new)
+    rows = cu.latents(n + 5, 11)               # five rows behind the last sequence
+    cache = torch.full((paged.pages, 64, cu.ROW), 0xA5, dtype=torch.uint8, device="cuda")
+    offs = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+    got = binding.q4_append(rows.cuda(), cache, paged.cuda, offs, torch.tensor(start, dtype=torch.int32).cuda())
+    assert got is cache
+    want = np.full((paged.pages * 64, cu.ROW), 0xA5, np.uint8)
+    at, q = 0, cu.quantise(rows[:n])
+    for b, k in enumerate(new):
+        for t in range(k):
+            want[paged.row(b, start[b] + t)] = q[at]
+            at += 1
+    np.testing.assert_array_equal(cache.cpu().numpy().reshape(-1, cu.ROW), want)
+
+
+def special_rows():
+    rows = cu.latents(12, 3).float()
+    rows[0, :] = 0.0
+    rows[1, :512] = torch.tensor(float("inf"))
+    rows[2, 40] = float("nan")
+    rows[3, :512] *= 2.0 ** -121            # around the smallest stored magnitude
+    rows[4, :512] *= 2.0 ** 118             # around the largest
+    rows[5, :32] = torch.arange(32) - 16.0  # ties: half steps of a scale of 16 / 7 rounded up
+    rows[6, :32] = torch.linspace(-7, 7, 32)
+    rows[6, 0] = 7.0                        # 7 times a scale exactly
+    rows[7, :32] = torch.tensor([7.0] + [k + 0.5 for k in range(-7, 7)] + [0.5] * 17)  # exact ties at scale 1
+    rows[8, 512:] = float("inf")
+    rows[9, 512:] = float("nan")
+    rows[10, 100] = -2.0 ** 120
+    rows[11, 100] = 2.0 ** 120 * (1 - 2.0 ** -8)
+    return rows.to(torch.bfloat16)
+
+
+def test_append_special_values():
+    rows = special_rows()
+    paged = cu.Paged([len(rows)])
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    binding.q4_append(rows.cuda(), cache, paged.cuda, torch.tensor([0, len(rows)], dtype=torch.int32).cuda(),
+                      torch.zeros(1, dtype=torch.int32).cuda())
+    got = cache.cpu().numpy().reshape(-1, cu.ROW)[paged.rows(0, range(len(rows)))]
+    want = cu.quantise(rows)
+    for r in range(len(rows)):
+        np.testing.assert_array_equal(got[r], want[r], err_msg=f"row {r}")
+
+
+def test_append_error_is_at_most_half_a_step():
+    rows = cu.latents(300, 5, std=3.0)
+    raw = cu.quantise(rows)
+    x, v = cu.f64(rows), cu.values(raw)
+    scale = cu.f64(torch.from_numpy(raw[:, 256:288].copy()).view(torch.bfloat16))
+    assert (np.abs(x - v)[:, :512] <= np.repeat(scale, 32, 1) / 2).all()
+    assert (x[:, 512:] == v[:, 512:]).all()
+
+
+def test_append_counts_rows_it_cannot_place():
+    paged = cu.Paged([64, 64, 64])
+    paged.table[1, 0] = -1
+    paged.table[2, 0] = paged.pages
+    rows = cu.latents(8, 7)
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    # sequence 0: positions 62 .. 65 (two past the table), 1: no page, 2: bad page
+    binding.q4_append(rows.cuda(), cache, paged.cuda, torch.tensor([0, 4, 6, 8], dtype=torch.int32).cuda(),
+                      torch.tensor([62, 0, 0], dtype=torch.int32).cuda())
+    assert binding.check_device(clear=True) == (5, 6)
+    got = cache.cpu().numpy().reshape(-1, cu.ROW)
+    at = paged.rows(0, [62, 63])
+    np.testing.assert_array_equal(got[at], cu.quantise(rows[:2]))
+    got[at] = 0
+    assert not got.any()
+    # negative start, and offsets that do not ascend: counted, nothing written
+    cache.zero_()
+    binding.q4_append(rows.cuda(), cache, paged.cuda[:2].contiguous(), torch.tensor([0, 5, 3], dtype=torch.int32).cuda(),
+                      torch.tensor([-9, -9], dtype=torch.int32).cuda())
+    st, bad = binding.check_device(clear=True)
+    assert st == 5 and bad == 3 and not cache.any()
+
+
+def test_append_then_read_on_another_stream_and_in_a_graph():
+    paged = cu.Paged([70, 3])
+    rows = cu.latents(73, 8).cuda()
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    offs, start = torch.tensor([0, 70, 73], dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    lists = torch.full((2, 71), -1, dtype=torch.int32)
+    lists[0, :70] = torch.randperm(70, generator=torch.Generator().manual_seed(1)).int()
+    lists[1, 68:] = torch.arange(3).int()
+    lists = lists.cuda()
+    table = paged.cuda
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    binding.q4_append(rows, cache, table, offs, start, stream=side)
+    out = binding.q4_read(cache, table, lists, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    want = cu.values(cu.quantise(rows.cpu()))
+    full = np.zeros((2, 71, 576))
+    full[0, :70] = want[:70][lists[0, :70].cpu().numpy()]
+    full[1, 68:] = want[70:]
+    np.testing.assert_array_equal(cu.f64(out), full)
+    graph, again = torch.cuda.CUDAGraph(), torch.empty_like(out)
+    cache.zero_()
+    with torch.cuda.graph(graph):
+        binding.q4_append(rows, cache, table, offs, start)
+        binding.q4_read(cache, table, lists, out=again)
+    for _ in range(2):
+        again.zero_()
+        graph.replay()
+        np.testing.assert_array_equal(cu.f64(again), full)
+
+
+def test_read_bad_positions_are_zero_rows_and_counted():
+    paged = cu.Paged([100])
+    cache, vals = fill(paged, [100], 4)
+    lists = torch.tensor([[0, -1, 128, -2, 99, 2**31 - 1]], dtype=torch.int32).cuda()
+    out = cu.f64(binding.q4_read(cache, paged.cuda, lists))
+    assert binding.check_device(clear=True) == (5, 3)
+    np.testing.assert_array_equal(out[0, [0, 4]], vals[paged.rows(0, [0, 99])])
+    assert not out[0, [1, 2, 3, 5]].any()
+
+
+# ---------------------------------------------------------------- sparse decode
+def lists_for(lens, T, K, seed, hole=0.0):
+    rng = np.random.default_rng(seed)
+    idx = np.full((len(lens), T, K), -1, np.int32)
+    for b, n in enumerate(lens):
+        for t in range(T):
+            k = min(n, K)
+            idx[b, t, :k] = rng.permutation(n)[:k]
+            idx[b, t, rng.random(K) < hole] = -1
+    return idx
+
+
+def run_sparse(lens, T, H, idx, nsplit, seed=0, what="", **kw):
+    paged = cu.Paged(lens, seed)
+    cache, vals = fill(paged, lens, seed + 1)
+    q = cu.queries(len(lens), T, H, seed + 2)
+    o, lse = binding.decode_q4(q.cuda(), cache, paged.cuda, torch.from_numpy(idx).cuda(), SCALE, nsplit, **kw)
+    torch.cuda.synchronize()
+    kv = lambda b, t: vals[paged.rows(b, idx[b, t][idx[b, t] >= 0])]
+    cu.check_attention(o, lse, q, kv, SCALE, what or f"H {H} K {idx.shape[2]} S {nsplit}")
+
+
+@pytest.mark.parametrize("H", [1, 3, 8, 15, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("nsplit", [0, 1, 3])
+def test_sparse_heads(H, nsplit):
+    run_sparse([300, 90], 2, H, lists_for([300, 90], 2, 130, H, hole=0.1), nsplit, seed=H)
+
+
+@pytest.mark.parametrize("K", [0, 1, 7, 31, 32, 33, 63, 64, 65, 127, 200, 513])
+@pytest.mark.parametrize("H,nsplit", [(16, 0), (16, 1), (16, 4), (64, 2), (5, 70)])
+def test_sparse_widths(K, H, nsplit):
+    run_sparse([600], 1, H, lists_for([600], 1, K, K), nsplit, seed=K + 1)
+
+
+@pytest.mark.parametrize("H", [8, 16, 48])
+def test_sparse_long_lists_cross_resolve_chunks(H):
+    run_sparse([5000, 4999], 1, H, lists_for([5000, 4999], 1, 4600, 3), 1, seed=5)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_sparse_duplicates_count_each_time(H):
+    idx = np.array([[[5, 5, 5, 9, -1, 9, 64, 5]]], np.int32)
+    run_sparse([70], 1, H, idx, 1)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("nsplit", [1, 3])
+def test_sparse_rows_that_select_nothing(H, nsplit):
+    idx = lists_for([200, 200, 200], 2, 100, 9)
+    idx[0, 1] = -1
+    idx[2] = -1
+    run_sparse([200, 200, 200], 2, H, idx, nsplit)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_sparse_bad_entries_are_masked_and_counted(H):
+    lens = [128]
+    paged = cu.Paged(lens, 2)
+    cache, vals = fill(paged, lens, 3)
+    idx = np.array([[[0, 5000, -7, 3, 127, 2**31 - 1]]], np.int32)
+    q = cu.queries(1, 1, H, 4)
+    o, lse = binding.decode_q4(q.cuda(), cache, paged.cuda, torch.from_numpy(idx).cuda(), SCALE, 1)
+    assert binding.check_device(clear=True) == (5, 3)
+    cu.check_attention(o, lse, q, lambda b, t: vals[paged.rows(0, [0, 3, 127])], SCALE, "bad entries")
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("nsplit", [1, 4])
+def test_a_row_without_a_finite_value_reaches_only_who_attends_to_it(H, nsplit):
+    """Row 10 was stored from infinities: token 0 selects it, token 1 does not."""
+    lens = [256]
+    paged = cu.Paged(lens, 2)
+    cache, vals = fill(paged, lens, 3)
+    bad = cu.latents(1, 1)
+    bad[0, 77] = float("inf")
+    binding.q4_append(bad.cuda(), cache, paged.cuda, torch.tensor([0, 1], dtype=torch.int32).cuda(),
+                      torch.tensor([10], dtype=torch.int32).cuda())
+    idx = lists_for(lens, 2, 150, 1)
+    idx[0][idx[0] == 10] = 11
+    idx[0, 0, 70] = 10
+    q = cu.queries(1, 2, H, 4)
+    o, lse = binding.decode_q4(q.cuda(), cache, paged.cuda, torch.from_numpy(idx).cuda(), SCALE, nsplit)
+    assert torch.isnan(o[0, 0]).all() and torch.isnan(lse[0, 0]).all()
+    ro, rl, to, tl = cu.attend(cu.f64(q)[0, 1], vals[paged.rows(0, idx[0, 1])], SCALE)
+    cu.check(o[0, 1], ro, to, "o")
+    cu.check(lse[0, 1], rl, tl, "lse")
+
+
+def test_sparse_on_another_stream_in_two_graphs_and_twice_the_same():
+    lens = [3000] * 4
+    paged = cu.Paged(lens, 2)
+    cache, vals = fill(paged, lens, 3)
+    table = paged.cuda
+    idx = lists_for(lens, 1, 700, 1)
+    q = cu.queries(4, 1, 16, 4)
+    qc, ic = q.cuda(), torch.from_numpy(idx).cuda()
+    o, lse = binding.decode_q4(qc, cache, table, ic, SCALE)
+    kv = lambda b, t: vals[paged.rows(b, idx[b, t])]
+    cu.check_attention(o, lse, q, kv, SCALE, "plain call")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = binding.decode_q4(qc, cache, table, ic, SCALE, stream=side)
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    graphs = []
+    for k in range(2):
+        g, out = torch.cuda.CUDAGraph(), (torch.empty_like(o), torch.empty_like(lse))
+        with torch.cuda.graph(g):
+            binding.decode_q4(qc, cache, table, ic, SCALE, o=out[0], lse=out[1])
+        graphs.append((g, out))
+    for g, out in graphs + graphs:
+        out[0].zero_()
+        g.replay()
+        assert torch.equal(o, out[0]) and torch.equal(lse, out[1])
+
+
+# ---------------------------------------------------------------- dense decode
+def run_dense(lens, H, nsplit, seed=0, K=None, slack=0):
+    lens = np.asarray(lens, np.int32)
+    paged = cu.Paged([int(x.max()) for x in lens], seed, extra=slack)
+    cache, vals = fill(paged, lens, seed + 1)
+    q = cu.queries(*lens.shape, H, seed + 2)
+    o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, torch.from_numpy(lens).cuda(), SCALE, nsplit, K=K)
+    torch.cuda.synchronize()
+    cu.check_attention(o, lse, q, lambda b, t: vals[paged.rows(b, range(lens[b, t]))], SCALE,
+                       f"H {H} S {nsplit} lens {lens.tolist()}")
+
+
+@pytest.mark.parametrize("H", [1, 7, 8, 16, 17, 32, 40, 64])
+@pytest.mark.parametrize("nsplit", [0, 1, 3])
+def test_dense_heads(H, nsplit):
+    run_dense([[198, 199, 200], [63, 64, 65]], H, nsplit, seed=H)
+
+
+@pytest.mark.parametrize("lens", [
+    [[0]], [[1]], [[0], [1], [0]], [[31], [32], [33]], [[63], [64], [65]], [[1000], [1], [129]],
+    [[0, 0, 5]], [[900, 3, 0, 64, 511]], [[128], [0], [2000], [0], [77]],
+])
+@pytest.mark.parametrize("H,nsplit", [(16, 0), (16, 5), (64, 0), (8, 1)])
+def test_dense_lengths(lens, H, nsplit):
+    run_dense(lens, H, nsplit, seed=len(lens))
+
+
+def test_dense_bound_above_every_length():
+    run_dense([[70], [300]], 16, 0, K=4096)
+    run_dense([[70], [300]], 64, 0, K=4096)
+
+
+@pytest.mark.parametrize("T,H", [(9, 8), (4, 16), (5, 3), (33, 2), (3, 64)])
+def test_dense_many_tokens(T, H):
+    run_dense([[500 - T + t + 1 for t in range(T)], [90 + t for t in range(T)]], H, 0, seed=T)
+
+
+def test_dense_clamps_and_counts_lengths_and_unmapped_positions():
+    paged = cu.Paged([128, 128], 1)
+    paged.table[1, 1] = -1
+    cache, vals = fill(paged, None, 2)
+    q = cu.queries(2, 1, 16, 3)
+    lens = torch.tensor([[-4], [128]], dtype=torch.int32).cuda()
+    o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, lens, SCALE, 1, K=128)
+    st, bad = binding.check_device(clear=True)
+    assert st == 5 and bad == 1 + 64
+    cu.check_attention(o, lse, q, lambda b, t: vals[paged.rows(b, range(64 * b))], SCALE, "unmapped")
+
+
+@pytest.mark.parametrize("H", [4, 64])
+def test_dense_a_draft_without_a_finite_value_leaves_earlier_tokens_alone(H):
+    paged = cu.Paged([100], 1)
+    cache, vals = fill(paged, None, 2)
+    bad = cu.latents(1, 1)
+    bad[0, 300] = float("nan")
+    binding.q4_append(bad.cuda(), cache, paged.cuda, torch.tensor([0, 1], dtype=torch.int32).cuda(),
+                      torch.tensor([99], dtype=torch.int32).cuda())
+    q = cu.queries(1, 2, H, 4)
+    lens = torch.tensor([[99, 100]], dtype=torch.int32).cuda()
+    o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, lens, SCALE, 0, K=100)
+    ro, rl, to, tl = cu.attend(cu.f64(q)[0, 0], vals[paged.rows(0, range(99))], SCALE)
+    cu.check(o[0, 0], ro, to, "o")
+    cu.check(lse[0, 0], rl, tl, "lse")
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]).all()
+
+
+def test_dense_equals_sparse_over_every_position():
+    """The same rows by a list and by a length: both are held to the same bound."""
+    lens = [700]
+    paged = cu.Paged(lens, 4)
+    cache, vals = fill(paged, lens, 5)
+    q = cu.queries(1, 1, 16, 6)
+    idx = torch.arange(700, dtype=torch.int32).view(1, 1, 700).cuda()
+    for o, lse in (binding.decode_q4(q.cuda(), cache, paged.cuda, idx, SCALE),
+                   binding.decode_dense_q4(q.cuda(), cache, paged.cuda, torch.tensor([[700]], dtype=torch.int32).cuda(), SCALE)):
+        cu.check_attention(o, lse, q, lambda b, t: vals[paged.rows(0, range(700))], SCALE, "both")
+
+
+@pytest.mark.parametrize("fill_value", [0.0, 1.0])
+def test_extreme_scores(fill_value):
+    """Scores of several hundred: one row takes all the weight; equal rows share it."""
+    paged = cu.Paged([64], 0)
+    rows = torch.full((64, 576), fill_value).to(torch.bfloat16)
+    rows[17] = 24.0
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    binding.q4_append(rows.cuda(), cache, paged.cuda, torch.tensor([0, 64], dtype=torch.int32).cuda(),
+                      torch.zeros(1, dtype=torch.int32).cuda())
+    vals = cu.values(cache.cpu().numpy().reshape(-1, cu.ROW))[paged.rows(0, range(64))]
+    for H in (16, 64):
+        q = torch.ones(1, 1, H, 576).to(torch.bfloat16)
+        o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, torch.tensor([[64]], dtype=torch.int32).cuda(), 1.0)
+        cu.check_attention(o, lse, q, lambda b, t: vals, 1.0, "extreme")
