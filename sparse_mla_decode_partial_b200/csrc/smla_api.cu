@@ -28,6 +28,7 @@
 #include "smla_partial_tc.cuh"
 #include "smla_indexer.cuh"
 #include "smla_evict.cuh"
+#include "smla_partial_q4.cuh"
 
 namespace {
 
@@ -1180,6 +1181,41 @@ void set_partials(PartialParams *p, void *workspace, size_t n) {
     p->part_lse = reinterpret_cast<float *>(ws + off_l);
 }
 
+// Query rows that smla_partial_q4.cuh takes at once.
+constexpr int kQ4Rows = smla::Q4Cfg::kRows;
+
+template <bool DIRECT>
+smla_status launch_q4_sparse(const PartialParams &p, int grid, cudaStream_t st) {
+    using C = smla::Q4Cfg;
+    if (p.H > kQ4Rows) return launch_tc<DIRECT, true>(p, grid, st);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_q4_sparse_kernel<DIRECT>), C::kSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = launch_dependent(smla::smla_q4_sparse_kernel<DIRECT>, grid, C::kThreads, C::kSmemBytes, st, p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+}
+
+// The dense schedule over packed units of at most kQ4Rows query rows.
+constexpr int kQ4MinTiles = 2;
+bool q4_dense_small(int T, int H) { return (long long)T * H <= kQ4Rows; }
+struct Q4Dense {
+    int pack, units;         // tokens per unit, units per sequence
+    long long n_units, ctas;
+    size_t off_ml, off_prefix, bytes;
+};
+Q4Dense q4_dense(int B, int T, int H, int nsplit) {
+    Q4Dense d{};
+    const int most = std::max(1, std::min(T, kQ4Rows / std::max(H, 1)));
+    d.units = (T + most - 1) / most;
+    d.pack = (T + d.units - 1) / d.units;
+    d.n_units = (long long)B * d.units;
+    d.ctas = d.n_units * nsplit;
+    const size_t rows = (size_t)(d.ctas + d.n_units) * kQ4Rows;
+    d.off_ml = round256(rows * smla::kDc * sizeof(float));
+    d.off_prefix = d.off_ml + round256(rows * sizeof(float2));
+    d.bytes = d.off_prefix + round256((size_t)(d.n_units + 1) * sizeof(int));
+    return d;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1235,7 +1271,8 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
 
 int smla_q4_nsplit(int B, int T, int H, int K) {
     if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
-    return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
+    if (H > kQ4Rows) return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
+    return smla_choose_nsplit(B, T, H, K, 0);
 }
 
 smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_pages,
@@ -1258,20 +1295,29 @@ smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_page
     if (nsplit == 1) {
         p.o = static_cast<__nv_bfloat16 *>(o);
         p.lse = lse;
-        return launch_tc<true, true>(p, (int)grid, s);
+        return launch_q4_sparse<true>(p, (int)grid, s);
     }
     if (workspace_bytes < smla_workspace_bytes(B, T, H, nsplit)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
     if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
     set_partials(&p, workspace, (size_t)B * T * H * nsplit);
-    st = launch_tc<false, true>(p, (int)grid, s);
+    st = launch_q4_sparse<false>(p, (int)grid, s);
     if (st != SMLA_OK) return st;
     return launch_combine(p.part_o, p.part_m, p.part_lse, B, T, H, nsplit, o, lse, s);
 }
 
-int smla_dense_q4_nsplit(int B, int T, int H, int K) { return smla_dense_nsplit(B, T, H, K); }
+int smla_dense_q4_nsplit(int B, int T, int H, int K) {
+    if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
+    if (!q4_dense_small(T, H)) return smla_dense_nsplit(B, T, H, K);
+    // one full wave of CTAs
+    const long long n = (long long)B * q4_dense(B, T, H, 1).units;
+    const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();
+    return (int)std::max<long long>(1, std::min<long long>(SMLA_MAX_NSPLIT, slots / n));
+}
 
 size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {
+    if (B < 0 || T < 0 || H < 0 || K < 0 || nsplit < 1 || nsplit > SMLA_MAX_NSPLIT) return 0;
+    if (q4_dense_small(T, H)) return q4_dense(B, T, H, nsplit).bytes;
     return smla_dense_workspace_bytes(B, T, H, K, nsplit);
 }
 
@@ -1287,11 +1333,44 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
     if (B == 0 || T == 0 || H == 0) return SMLA_OK;
     if (o == nullptr || lse == nullptr) return SMLA_ERR_INVALID_ARG;
     if (!aligned(o, 16) || !aligned(lse, 4)) return SMLA_ERR_MISALIGNED;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (q4_dense_small(T, H)) {
+        if (nsplit == 0) nsplit = smla_dense_q4_nsplit(B, T, H, K);
+        const Q4Dense d = q4_dense(B, T, H, nsplit);
+        if (d.ctas + d.n_units > INT_MAX / kQ4Rows || d.n_units * ((K + 63ll) / 64) > INT_MAX)
+            return SMLA_ERR_INVALID_ARG;
+        if (workspace_bytes < d.bytes) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+        if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
+        if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
+        smla::Q4Params a{};
+        a.p = make_params(q, cache_q4, num_pages, page_table, pt_stride, nullptr, B, d.units, d.pack * H, K,
+                          scale, 1);
+        a.p.seq_lens = seq_lens;
+        a.p.pack = d.pack;
+        a.p.dense_t = T;
+        a.p.dense_h = H;
+        a.p.o = static_cast<__nv_bfloat16 *>(o);
+        a.p.lse = lse;
+        a.dense = 1;
+        a.grid = (int)d.ctas;
+        a.min_tiles = kQ4MinTiles;
+        a.n_units = (int)d.n_units;
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        a.piece_o = reinterpret_cast<float *>(ws);
+        a.piece_ml = reinterpret_cast<float2 *>(ws + d.off_ml);
+        a.prefix = reinterpret_cast<int *>(ws + d.off_prefix);
+        using C = smla::Q4Cfg;
+        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_q4_dense_kernel), C::kSmemBytes);
+        if (e != cudaSuccess) return cuda_fail(e);
+        e = launch_dependent(smla::smla_q4_dense_kernel, a.grid, C::kThreads, C::kSmemBytes, s, a);
+        if (e != cudaSuccess) return cuda_fail(e);
+        e = launch_dependent(smla::smla_q4_combine_kernel, B * T * H, smla::kQ4CombineThreads, 0, s, a);
+        return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+    }
     DensePlan d = dense_plan(B, T, H, K, nsplit);
     const int kc64 = K > 0 ? ((K + d.nsplit - 1) / d.nsplit + 63) / 64 * 64 : 0;
     if (K > 0) d.nsplit = (K + kc64 - 1) / kc64;
     if ((long long)B * d.units * d.nsplit > INT_MAX) return SMLA_ERR_INVALID_ARG;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     PartialParams p = dense_params(q, cache_q4, num_pages, page_table, pt_stride, seq_lens, B, T, H, K,
                                    scale, d);
     if (K > 0) p.kc = kc64;

@@ -1,0 +1,710 @@
+// smla_partial_q4.cuh -- split-K partial pass over 4-bit cache rows for up to
+// 16 query rows (heads of one token, or of several tokens that share a dense
+// prefix), and the combine of the dense schedule's pieces.
+//
+// At 416 bytes a row the memory can deliver one row per SM about every 18
+// cycles, so what counts is the work per row: decoding 512 codes, 2 * 16 * 1088
+// flop, and the shared-memory traffic of both.  Writing decoded bf16 rows to
+// shared memory for the tensor core to read (as the tcgen05 kernel does) costs
+// 9 cycles of store and 17 of operand reads per row and leaves 3/4 of its M
+// rows empty; here the codes stay packed in shared memory and are decoded in
+// registers, straight into mma.sync B fragments, once per product:
+//   S = Q K^T   A = 16 query rows (fragments in shared memory, in lane order),
+//               B = 8 cache rows: a lane takes a whole group of 32 codes of one
+//               row (one 16-byte load, one scale) for eight k16 steps; the
+//               order of the dims within the sum is free.
+//   O += P C    B = 16 cache rows x 8 columns: a lane takes 16 columns of four
+//               rows; two byte permutes interleave the codes of two rows, and
+//               the same and/or + fma as above then gives row pairs.
+// A CTA is four warps and works on tiles of 64 rows.  Warp w scores rows 16 w
+// .. 16 w + 15 alone (all 576 dims: no exchange of partial scores) and leaves
+// P as an A fragment in its own rows' spent rope bytes; after one barrier every
+// warp reads all four fragments and accumulates its 128 output columns.
+// Running maxima: each warp keeps one per query row over its own rows, rounded
+// up to an integer (log2 units), so that bringing its P to the common maximum
+// is a multiplication by a power of two, exact in bf16: P is rounded once.
+// Rows 416 bytes apart: the lane-to-row map below keeps every shared load free
+// of bank conflicts without padding, so a page of the cache lands by one bulk
+// copy.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "smla_indexer.cuh"
+#include "smla_q4.cuh"
+#include "smla_tc_ptx.cuh"
+
+namespace smla {
+
+struct Q4Cfg {
+    static constexpr int kThreads = 128;
+    static constexpr int kRows = 16;                       // query rows (the mma's M)
+    static constexpr int kTile = 64;                       // cache rows: one page
+    static constexpr int kStages = 2;
+    static constexpr int kStageBytes = kTile * kQ4RowBytes;  // 26624
+    static constexpr int kResolve = 512;                   // list entries resolved at a time
+    static constexpr int kOffQ = 0;                        // uint4 [36][32]
+    static constexpr int kOffStage = 36 * 512;
+    static constexpr int kOffRows = kOffStage + kStages * kStageBytes;  // int [kResolve]
+    static constexpr int kOffBar = kOffRows + kResolve * 4;
+    static constexpr int kSmemBytes = kOffBar + 8 * kStages;
+    static constexpr int kMinBlocks = 3;                   // per SM: 3 x (73.8 + 1) KB
+};
+static_assert(Q4Cfg::kMinBlocks * (Q4Cfg::kSmemBytes + 1024) <= 233472, "shared memory per SM");
+
+// The dense schedule: units (packed query tokens of one sequence) have
+// ceil(longest visible length / 64) tiles; CTA c of `grid` takes an equal run
+// of the flattened tiles and writes one piece per unit it meets, piece (c, u)
+// at slot c + u (c + u grows strictly along the run, so slots are distinct).
+struct Q4Params {
+    PartialParams p;
+    int dense;
+    int grid;          // dense: CTAs that share the tiles
+    int min_tiles;     // dense: fewest tiles worth a CTA
+    int *prefix;       // dense: [n_units + 1] tiles before each unit, written by CTA 0
+    int n_units;
+    float *piece_o;    // [grid + n_units, 16, 512]
+    float2 *piece_ml;  // [grid + n_units, 16]: (max, lse) in log2 units
+};
+
+// Cache row (0..7 of its n8 tile) that column n of a B fragment stands for.
+// With rows 416 = 3 * 128 + 32 bytes apart, rows 2 m and 2 m + 1 of the score
+// product lie 64 bytes apart modulo 128, and rows 0, 2, 4, 6 (or 1, 3, 5, 7) of
+// the output product in four different 32-byte quarters.
+__device__ __forceinline__ int q4_row_of(int n) {
+    const int c = n >> 1;
+    return (n & 1) ? 4 + ((c + 2) & 3) : c;
+}
+
+// First of the four dims that lane column c feeds to k16 step s of the score
+// product (dims +0, +1 at k = 2 c, 2 c + 1 and +2, +3 at k = 2 c + 8, 2 c + 9).
+__device__ __forceinline__ int q4_dim_of(int s, int c) {
+    return s < 32 ? 32 * (4 * (s >> 3) + c) + 8 * ((s & 7) >> 1) + 4 * (s & 1)
+                  : 32 * (s >> 1) + 8 * c + 4 * (s & 1);
+}
+
+__device__ __forceinline__ uint32_t lds_u16x2(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return (uint32_t)v * 0x00010001u;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint4 lds_16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds_8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts_f(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts_16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 2^d as a pair of bf16 for an integer-valued d <= 0 (0 below 2^-126, and for
+// d = -inf or NaN, which stand for a side that has seen nothing).
+__device__ __forceinline__ uint32_t bf16x2_pow2(float d) {
+    const int e = 127 + (int)fmaxf(d, -127.f);
+    return (uint32_t)(e << 7) * 0x00010001u;
+}
+
+// One warp's share of a CTA: scores of 16 rows, 128 output columns.
+struct Q4Consumer {
+    int warp, lane, r, c;
+    float oacc[16][4];
+    float mw0, mw1;    // running max (an integer or -inf) of query rows r, r + 8 over this warp's cache rows
+    float l0, l1;      // this lane's part of sum exp2(s - mw)
+    float M0, M1;      // the CTA's running max, what oacc is relative to
+
+    __device__ __forceinline__ void init(int warp_, int lane_) {
+        warp = warp_;
+        lane = lane_;
+        r = lane >> 2;
+        c = lane & 3;
+        reset();
+    }
+    __device__ __forceinline__ void reset() {
+        mw0 = mw1 = M0 = M1 = -INFINITY;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
+    }
+
+    // Raw scores of this warp's 16 rows against 16 query rows.
+    __device__ __forceinline__ void scores(uint32_t q_addr, uint32_t tile, float (&s)[2][4]) {
+        const uint32_t row = tile + (16 * warp + q4_row_of(r)) * kQ4RowBytes;
+        const uint32_t q = q_addr + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t s2[2], bias[2];
+            uint4 code[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                code[i] = lds_16(row + i * 8 * kQ4RowBytes + 16 * (4 * j + c));
+                s2[i] = lds_u16x2(row + i * 8 * kQ4RowBytes + kQ4OffScale + 2 * (4 * j + c));
+                bias[i] = q4_bias(s2[i]);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint4 a0 = lds_16(q + (8 * j + 2 * w) * 512);
+                const uint4 a1 = lds_16(q + (8 * j + 2 * w + 1) * 512);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t word = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
+                    const uint4 v = q4_word(word, s2[i], bias[i]);
+                    mma_bf16_16816(s[i], a0.x, a0.y, a0.z, a0.w, v.x, v.y);
+                    mma_bf16_16816(s[i], a1.x, a1.y, a1.z, a1.w, v.z, v.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 a0 = lds_16(q + (32 + 2 * j) * 512), a1 = lds_16(q + (33 + 2 * j) * 512);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = lds_16(row + i * 8 * kQ4RowBytes + kQ4OffRope + 64 * j + 16 * c);
+                mma_bf16_16816(s[i], a0.x, a0.y, a0.z, a0.w, v.x, v.y);
+                mma_bf16_16816(s[i], a1.x, a1.y, a1.z, a1.w, v.z, v.w);
+            }
+        }
+    }
+
+    // Masked scores (log2 units, -inf where masked) -> P in this warp's rows'
+    // rope bytes: its A fragment, and the maxima it is relative to.
+    __device__ __forceinline__ void softmax(uint32_t tile, float (&s)[2][4]) {
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        const float n0 = fmaxf(mw0, ceilf(x0)), n1 = fmaxf(mw1, ceilf(x1));
+        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+        l0 *= fast_exp2(mw0 - u0);  // 2^-inf = 0 before the first visible row
+        l1 *= fast_exp2(mw1 - u1);
+        mw0 = n0;
+        mw1 = n1;
+        uint32_t a[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float p00 = fast_exp2(s[i][0] - u0), p01 = fast_exp2(s[i][1] - u0);
+            const float p10 = fast_exp2(s[i][2] - u1), p11 = fast_exp2(s[i][3] - u1);
+            l0 += p00 + p01;
+            l1 += p10 + p11;
+            a[2 * i] = pack_bf16x2(p00, p01);
+            a[2 * i + 1] = pack_bf16x2(p10, p11);
+        }
+        __syncwarp();  // every lane has read the rope bytes
+        const uint32_t mine = tile + 16 * warp * kQ4RowBytes + kQ4OffRope;
+        sts_16(mine + (lane >> 1) * kQ4RowBytes + 16 * (lane & 1), a[0], a[1], a[2], a[3]);
+        if (c == 0) {
+            sts_f(mine + r * kQ4RowBytes + 32, mw0);
+            sts_f(mine + (r + 8) * kQ4RowBytes + 32, mw1);
+        }
+    }
+
+    // O += P C over the tile's 64 rows, this warp's 128 columns.
+    __device__ __forceinline__ void output(uint32_t tile) {
+        float m0[4], m1[4];
+        float n0 = M0, n1 = M1;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t at = tile + 16 * w * kQ4RowBytes + kQ4OffRope + 32;
+            m0[w] = lds_f(at + r * kQ4RowBytes);
+            m1[w] = lds_f(at + (r + 8) * kQ4RowBytes);
+            n0 = fmaxf(n0, m0[w]);
+            n1 = fmaxf(n1, m1[w]);
+        }
+        if (__any_sync(0xffffffffu, n0 != M0 || n1 != M1)) {
+            const float a0 = n0 == M0 ? 1.f : fast_exp2(M0 - n0), a1 = n1 == M1 ? 1.f : fast_exp2(M1 - n1);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                oacc[n][0] *= a0;
+                oacc[n][1] *= a0;
+                oacc[n][2] *= a1;
+                oacc[n][3] *= a1;
+            }
+            M0 = n0;
+            M1 = n1;
+        }
+        const int ra = q4_row_of(2 * c), rb = q4_row_of(2 * c + 1);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t base = tile + 16 * w * kQ4RowBytes;
+            const uint4 pf = lds_16(base + (lane >> 1) * kQ4RowBytes + kQ4OffRope + 16 * (lane & 1));
+            const uint32_t f0 = bf16x2_pow2(m0[w] - M0), f1 = bf16x2_pow2(m1[w] - M1);
+            const uint32_t a0 = bf16x2_mul(pf.x, f0), a1 = bf16x2_mul(pf.y, f1);
+            const uint32_t a2 = bf16x2_mul(pf.z, f0), a3 = bf16x2_mul(pf.w, f1);
+            const uint32_t at_a = base + ra * kQ4RowBytes, at_b = base + rb * kQ4RowBytes;
+            const uint32_t col = 64 * warp + 8 * r, grp = kQ4OffScale + 2 * (4 * warp + (r >> 1));
+            const uint2 wa = lds_8(at_a + col), wb = lds_8(at_b + col);
+            const uint2 va = lds_8(at_a + 8 * kQ4RowBytes + col), vb = lds_8(at_b + 8 * kQ4RowBytes + col);
+            const uint32_t s2 = lds_u16(at_a + grp) | lds_u16(at_b + grp) << 16;
+            const uint32_t t2 = lds_u16(at_a + 8 * kQ4RowBytes + grp) | lds_u16(at_b + 8 * kQ4RowBytes + grp) << 16;
+            const uint32_t sb = q4_bias(s2), tb = q4_bias(t2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t x = i ? wa.y : wa.x, y = i ? wb.y : wb.x;
+                const uint32_t z = i ? va.y : va.x, u = i ? vb.y : vb.x;
+                // low halves: values 0, 2, 4, 6 of both rows; high halves: 1, 3, 5, 7
+                const uint32_t e0 = __byte_perm(x, y, 0x5410), o0 = __byte_perm(x, y, 0x7632);
+                const uint32_t e1 = __byte_perm(z, u, 0x5410), o1 = __byte_perm(z, u, 0x7632);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mma_bf16_16816(oacc[8 * i + 2 * k], a0, a1, a2, a3, q4_pair(e0 >> (4 * k), s2, sb),
+                                   q4_pair(e1 >> (4 * k), t2, tb));
+                    mma_bf16_16816(oacc[8 * i + 2 * k + 1], a0, a1, a2, a3, q4_pair(o0 >> (4 * k), s2, sb),
+                                   q4_pair(o1 >> (4 * k), t2, tb));
+                }
+            }
+        }
+    }
+
+    // Total weight of query rows r, r + 8 relative to M, the same in every lane
+    // of a row.  scratch: float2 [4][16] in shared memory; the CTA synchronises.
+    __device__ __forceinline__ void totals(float2 *scratch, float &t0, float &t1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if (c == 0) {
+            scratch[16 * warp + r] = make_float2(mw0, l0);
+            scratch[16 * warp + r + 8] = make_float2(mw1, l1);
+        }
+        __syncthreads();
+        t0 = t1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 x = scratch[16 * w + r], y = scratch[16 * w + r + 8];
+            // a warp that saw nothing has l = 0; one whose every score was NaN
+            // keeps its NaN
+            t0 += x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - M0);
+            t1 += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M1);
+        }
+    }
+};
+
+// Stage 16 query rows (row0 .. row0 + nrows - 1 of q; the rest zero) as A
+// fragments in lane order.
+__device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q, long long row0, int nrows) {
+    uint4 *frag = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+    for (int k = 0; k < 9; ++k) {
+        const int i = threadIdx.x + 128 * k, l = i & 31, st = i >> 5, r = l >> 2;
+        const __nv_bfloat16 *src = q + (row0 + r) * kD + q4_dim_of(st, l & 3);
+        uint2 lo = make_uint2(0u, 0u), hi = lo;
+        if (r < nrows)
+            asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(lo.x), "=r"(lo.y) : "l"(src));
+        if (r + 8 < nrows)
+            asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(hi.x), "=r"(hi.y) : "l"(src + 8 * kD));
+        frag[i] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+    }
+}
+
+// ---------------------------------------------------------------- sparse lists
+// One CTA = one (query token, split).  Equal splits; the partials go to
+// part_o / part_m / part_lse [B, T, H, S] (DIRECT: o, lse).
+template <bool DIRECT>
+__global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sparse_kernel(const PartialParams p) {
+    using C = Q4Cfg;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int s = blockIdx.x % p.nsplit, bt = blockIdx.x / p.nsplit;
+    const int j0 = (int)min((long long)s * p.kc, (long long)p.K);
+    const int len = (int)min((long long)p.kc, (long long)p.K - j0);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    int *rows_s = reinterpret_cast<int *>(smem + C::kOffRows);
+    const uint32_t sbase = smem_addr(smem);
+    bool dead = false;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], C::kThreads);
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint8_t *cache = reinterpret_cast<const uint8_t *>(p.cache);
+
+    // 26 16-byte pieces per row, 13 per thread and tile; padding slots are
+    // zero-filled (scale 0: they decode to zeros)
+    auto issue = [&](int it, int t, int n) {
+        const uint32_t dst = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
+#pragma unroll
+        for (int k = 0; k < 13; ++k) {
+            const int e = tid + 128 * k, row = e / 26, ch = e - 26 * row;
+            const int j = t * C::kTile + row;
+            const int at = j < n ? rows_s[j] : -1;
+            const uint8_t *src = cache + (size_t)(at >= 0 ? at : 0) * kQ4RowBytes + 16 * ch;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * e), "l"(src),
+                         "r"(at >= 0 ? 16u : 0u)
+                         : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[it & 1]))
+                     : "memory");
+    };
+
+    Q4Consumer w;
+    w.init(warp, lane);
+    bool staged = false;
+    int it = 0;  // tiles so far: ring position
+    for (int base = 0; base < len; base += C::kResolve) {
+        const int n = min(C::kResolve, len - base);
+        __syncthreads();  // the ring and rows_s are free
+        resolve_rows<4>(p, bt, j0, base, n, rows_s, tid, C::kThreads);
+        __syncthreads();
+        const int tiles = (n + C::kTile - 1) / C::kTile;
+        issue(it, 0, n);
+        if (!staged) {
+            q4_stage_q(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
+            staged = true;
+            __syncthreads();
+        }
+        for (int t = 0; t < tiles; ++t, ++it) {
+            const uint32_t tile = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
+            if (t + 1 < tiles && t == 0) issue(it + 1, 1, n);
+            mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
+            float sc[2][4];
+            w.scores(sbase + C::kOffQ, tile, sc);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = t * C::kTile + 16 * warp + 8 * i + q4_row_of(2 * w.c + e);
+                    const bool on = j < n && rows_s[j] >= 0;
+                    sc[i][e] = on ? sc[i][e] * p.scale_log2 : -INFINITY;
+                    sc[i][2 + e] = on ? sc[i][2 + e] * p.scale_log2 : -INFINITY;
+                }
+            }
+            w.softmax(tile, sc);
+            __syncthreads();  // P complete; every warp is done with the previous tile
+            if (t >= 1 && t + 1 < tiles) issue(it + 1, t + 1, n);
+            w.output(tile);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float t0, t1;
+    w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int h = w.r + 8 * half;
+        if (h >= p.H) continue;
+        const float tot = half ? t1 : t0, M = half ? w.M1 : w.M0;
+        const bool some = !(tot == 0.f);  // NaN counts
+        const size_t row = (size_t)bt * p.H + h;
+        const float inv = !DIRECT ? 1.f : some ? 1.f / tot : 0.f;
+        // n8 tile n of the accumulators is column 128 warp + 16 (2 c + e) + n
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = 128 * warp + 32 * w.c + 16 * e;
+            if (DIRECT) {
+#pragma unroll
+                for (int n = 0; n < 16; n += 8) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] = pack_bf16x2(w.oacc[n + 2 * k][2 * half + e] * inv, w.oacc[n + 2 * k + 1][2 * half + e] * inv);
+                    *reinterpret_cast<uint4 *>(p.o + row * kDc + col + n) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 16; n += 4)
+                    *reinterpret_cast<float4 *>(p.part_o + (row * p.nsplit + s) * kDc + col + n) =
+                        make_float4(w.oacc[n][2 * half + e], w.oacc[n + 1][2 * half + e], w.oacc[n + 2][2 * half + e],
+                                    w.oacc[n + 3][2 * half + e]);
+            }
+        }
+        if (warp == 0 && w.c == 0) {
+            const float base = M == -INFINITY ? 0.f : M;
+            const float lse = some ? (base + log2f(tot)) * kLn2 : -INFINITY;
+            if (DIRECT) {
+                p.lse[row] = lse;
+            } else {
+                p.part_m[row * p.nsplit + s] = some ? base * kLn2 : -INFINITY;
+                p.part_lse[row * p.nsplit + s] = lse;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dense prefixes
+// Longest visible length of unit u's query tokens; lengths outside [0, K] are
+// clamped (and counted when `count`).
+__device__ __forceinline__ int q4_unit_len(const PartialParams &p, int u, bool count) {
+    const int b = u / p.T, t0 = (u - b * p.T) * p.pack, t1 = min(t0 + p.pack, p.dense_t);
+    int len = 0;
+    for (int t = t0; t < t1; ++t) {
+        const int raw = ld_input(p.seq_lens + (size_t)b * p.dense_t + t);
+        if (count && (raw < 0 || raw > p.K)) count_bad_index();
+        len = max(len, min(max(raw, 0), p.K));
+    }
+    return len;
+}
+
+// CTAs that share `total` tiles.
+__host__ __device__ __forceinline__ int q4_sharers(int grid, int min_tiles, long long total) {
+    const long long most = (total + min_tiles - 1) / min_tiles;
+    return (int)(most < 1 ? 1 : most < grid ? most : grid);
+}
+
+__global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_dense_kernel(const Q4Params a) {
+    using C = Q4Cfg;
+    const PartialParams &p = a.p;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    int *scratch = reinterpret_cast<int *>(smem + C::kOffRows);  // scan scratch, then what the scan found
+    const uint32_t sbase = smem_addr(smem);
+    bool dead = false;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- this CTA's run of tiles: total first, then the unit it starts in
+    long long total = 0;
+    for (int u0 = 0; u0 < a.n_units; u0 += C::kThreads) {
+        const int u = u0 + tid;
+        const int tiles = u < a.n_units ? (q4_unit_len(p, u, blockIdx.x == 0) + C::kTile - 1) / C::kTile : 0;
+        int sum;
+        const int incl = ix_block_scan(tiles, scratch, &sum);
+        if (blockIdx.x == 0 && u < a.n_units) a.prefix[u] = (int)total + incl - tiles;
+        total += sum;
+    }
+    if (blockIdx.x == 0 && tid == 0) a.prefix[a.n_units] = (int)total;
+    const int sharers = q4_sharers(a.grid, a.min_tiles, total);
+    if ((int)blockIdx.x >= sharers || total == 0) return;
+    const long long begin = total * blockIdx.x / sharers, end = total * (blockIdx.x + 1) / sharers;
+    long long before = 0;
+    for (int u0 = 0; u0 < a.n_units; u0 += C::kThreads) {
+        const int u = u0 + tid;
+        const int tiles = u < a.n_units ? (q4_unit_len(p, u, false) + C::kTile - 1) / C::kTile : 0;
+        int sum;
+        const int incl = ix_block_scan(tiles, scratch, &sum);
+        const long long first = before + incl - tiles;
+        if (first <= begin && begin < first + tiles) {
+            scratch[40] = u;
+            scratch[41] = (int)(begin - first);
+        }
+        before += sum;
+        if (before > begin) break;
+    }
+    __syncthreads();
+    int unit = scratch[40], tile0 = scratch[41];
+    const uint8_t *cache = reinterpret_cast<const uint8_t *>(p.cache);
+    const long long max_pos = (long long)p.pt_stride * kPage;
+
+    Q4Consumer w;
+    w.init(warp, lane);
+    int it = 0;
+    for (long long at = begin; at < end; ++unit, tile0 = 0) {
+        const int len = q4_unit_len(p, unit, false);
+        const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), end - at);
+        if (tiles <= 0) continue;  // a unit that sees nothing
+        at += tiles;
+        const int b = unit / p.T, tok0 = (unit - b * p.T) * p.pack;
+        const int nrows = min(p.pack, p.dense_t - tok0) * p.dense_h;
+        const long long row0 = ((long long)b * p.dense_t + tok0) * p.dense_h;
+        const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
+        // page of this unit's tile t, -1 where none is mapped
+        auto page_of = [&](int t) {
+            if ((long long)t * kPage >= max_pos) return -1;
+            const int pg = ld_input(pt_b + t);
+            return (pg >= 0 && (long long)pg < p.num_pages) ? pg : -1;
+        };
+        auto issue = [&](int i, int pg) {  // thread 0
+            uint64_t *bar = &full[i & 1];
+            if (pg < 0) {
+                mbar_arrive(bar);  // nothing to copy
+                return;
+            }
+            mbar_arrive_expect_tx(bar, (uint32_t)C::kStageBytes);
+            bulk_g2s(smem + C::kOffStage + (i & 1) * C::kStageBytes,
+                     cache + (size_t)pg * (kPage * kQ4RowBytes), (uint32_t)C::kStageBytes, bar);
+        };
+        fence_proxy_async_smem();
+        __syncthreads();  // the previous piece is done with the ring and with Q
+        if (tid == 0) {
+            issue(it, page_of(tile0));
+            if (tiles > 1) issue(it + 1, page_of(tile0 + 1));
+        }
+        q4_stage_q(smem + C::kOffQ, p.q, row0, nrows);
+        // visible positions of this lane's two query rows
+        int lim0 = 0, lim1 = 0;
+        if (w.r < nrows)
+            lim0 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + tok0 + w.r / p.dense_h), 0), p.K);
+        if (w.r + 8 < nrows)
+            lim1 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + tok0 + (w.r + 8) / p.dense_h), 0), p.K);
+        w.reset();
+        __syncthreads();
+        for (int t = 0; t < tiles; ++t, ++it) {
+            const uint32_t tile = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
+            const int pos0 = (tile0 + t) * C::kTile;
+            const bool mapped = page_of(tile0 + t) >= 0;
+            int next = -1;
+            if (tid == 0 && t >= 1 && t + 1 < tiles) next = page_of(tile0 + t + 1);
+            mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
+            // rows that no query token sees may hold anything: scale 0 makes
+            // them decode to zeros (0 * P = 0)
+            const int live = mapped ? min(len - pos0, C::kTile) : 0;
+            if (live < C::kTile) {
+                if (!mapped && tid < min(len - pos0, C::kTile)) count_bad_index();
+                if (tid >= live && tid < C::kTile) {
+                    const uint32_t sc = tile + tid * kQ4RowBytes + kQ4OffScale;
+                    sts_16(sc, 0u, 0u, 0u, 0u);
+                    sts_16(sc + 16, 0u, 0u, 0u, 0u);
+                }
+                __syncthreads();
+            }
+            float sc[2][4];
+            w.scores(sbase + C::kOffQ, tile, sc);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 16 * warp + 8 * i + q4_row_of(2 * w.c + e);
+                    const int pos = j < live ? pos0 + j : INT_MAX;
+                    sc[i][e] = pos < lim0 ? sc[i][e] * p.scale_log2 : -INFINITY;
+                    sc[i][2 + e] = pos < lim1 ? sc[i][2 + e] * p.scale_log2 : -INFINITY;
+                }
+            }
+            w.softmax(tile, sc);
+            fence_proxy_async_smem();  // P and cleared scales, before a later bulk copy writes there
+            __syncthreads();  // P complete; every warp is done with the previous tile
+            if (tid == 0 && t >= 1 && t + 1 < tiles) issue(it + 1, next);
+            w.output(tile);
+        }
+        // ---- the piece
+        __syncthreads();
+        float t0, t1;
+        w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1);
+        const size_t slot = (size_t)blockIdx.x + unit;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int h = w.r + 8 * half;
+            if (h >= nrows) continue;
+            float *dst = a.piece_o + (slot * C::kRows + h) * kDc + 128 * warp + 32 * w.c;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int n = 0; n < 16; n += 4)
+                    *reinterpret_cast<float4 *>(dst + 16 * e + n) =
+                        make_float4(w.oacc[n][2 * half + e], w.oacc[n + 1][2 * half + e], w.oacc[n + 2][2 * half + e],
+                                    w.oacc[n + 3][2 * half + e]);
+            if (warp == 0 && w.c == 0) {
+                const float tot = half ? t1 : t0, M = half ? w.M1 : w.M0;
+                const bool some = !(tot == 0.f);
+                const float base = M == -INFINITY ? 0.f : M;
+                a.piece_ml[slot * C::kRows + h] =
+                    some ? make_float2(base, base + log2f(tot)) : make_float2(-INFINITY, -INFINITY);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine of pieces
+// One CTA per query row: o = sum_c 2^(m_c - M) O_c / L, L = sum_c 2^(lse_c - M),
+// lse = M + log2 L, over the pieces c that the row's unit was cut into.
+// 128 threads hold the 512 columns as float4; four groups of them take every
+// fourth piece and meet in shared memory.
+constexpr int kQ4CombineThreads = 512;
+__global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(const Q4Params a) {
+    __shared__ float4 part[3][128];
+    __shared__ float warp_max[16], warp_sum[16];
+    const PartialParams &p = a.p;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const long long row = blockIdx.x;  // of [B, T, H]
+    const int h = (int)(row % p.dense_h);
+    const long long tok = row / p.dense_h;
+    const int b = (int)(tok / p.dense_t), t = (int)(tok - (long long)b * p.dense_t);
+    const int unit = b * p.T + t / p.pack, r = (t % p.pack) * p.dense_h + h;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long first = ld_input(a.prefix + unit), last = ld_input(a.prefix + unit + 1);
+    const long long total = ld_input(a.prefix + a.n_units);
+    const int sharers = q4_sharers(a.grid, a.min_tiles, total);
+    // CTA of flattened tile x: the c with total c / sharers <= x < total (c + 1) / sharers
+    int c0 = 0, n = 0;
+    if (last > first) {
+        c0 = (int)(((first + 1) * sharers - 1) / total);
+        n = (int)((last * sharers - 1) / total) - c0 + 1;
+    }
+    const float2 *ml = a.piece_ml + ((size_t)c0 + unit) * Q4Cfg::kRows + r;
+    const float *po = a.piece_o + (((size_t)c0 + unit) * Q4Cfg::kRows + r) * kDc;
+    float M = -INFINITY;
+    for (int c = tid; c < n; c += kQ4CombineThreads) M = fmaxf(M, __ldcg(ml + (size_t)c * Q4Cfg::kRows).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) warp_max[warp] = M;
+    __syncthreads();
+    M = warp_max[lane & 15];
+#pragma unroll
+    for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    __nv_bfloat16 *out = p.o + row * kDc;
+    if (M == -INFINITY) {  // nothing attended to
+        if (tid < 128) *reinterpret_cast<uint2 *>(out + 4 * tid) = make_uint2(0u, 0u);
+        if (tid == 0) p.lse[row] = -INFINITY;
+        return;
+    }
+    float L = 0.f;
+    for (int c = tid; c < n; c += kQ4CombineThreads) {
+        const float v = __ldcg(ml + (size_t)c * Q4Cfg::kRows).y;
+        if (v != -INFINITY) L += exp2f(v - M);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) warp_sum[warp] = L;
+    const int g = tid >> 7, col = tid & 127;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = g; c < n; c += 4) {
+        const float m = __ldcg(ml + (size_t)c * Q4Cfg::kRows).x;
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + (size_t)c * Q4Cfg::kRows * kDc) + col);
+        if (m == -INFINITY) continue;  // an empty piece
+        const float f = exp2f(m - M);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+    }
+    if (g > 0) part[g - 1][col] = acc;
+    __syncthreads();
+    if (g > 0) return;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) L += warp_sum[w];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const float4 v = part[k][col];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+    }
+    const float inv = 1.f / L;
+    *reinterpret_cast<uint2 *>(out + 4 * col) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (tid == 0) p.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+}  // namespace smla

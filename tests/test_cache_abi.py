@@ -115,7 +115,10 @@ def test_workspace_sizes_and_splits(lib):
     r = lambda x: (x + 255) // 256 * 256
     assert binding.evict_workspace_bytes(3, 1000) == r(3 * 1000 * 4)
     assert binding.evict_workspace_bytes(-1, 5) == 0
-    assert binding.dense_q4_workspace_bytes(2, 1, 16, 4096, 1) == 0
+    assert binding.dense_q4_workspace_bytes(2, 1, 64, 4096, 1) == 0
+    assert binding.dense_q4_workspace_bytes(2, 3, 8, 4096, 5) == binding.workspace_bytes(2, 3, 8, 5)
+    for S in (1, 7):  # up to 16 query rows: pieces of (splits + 1) per unit, their maxima, the tiles before each unit
+        assert binding.dense_q4_workspace_bytes(3, 2, 8, 4096, S) == r(3 * (S + 1) * 16 * 2048) + r(3 * (S + 1) * 16 * 8) + r(16)
     assert binding.dense_q4_workspace_bytes(2, 1, 16, 4096, 0) == 0
     for B, T, H, K in [(1, 1, 16, 2048), (64, 1, 16, 2048), (60, 1, 64, 2048), (3, 5, 8, 1999)]:
         assert 1 <= binding.q4_nsplit(B, T, H, K) <= 1024
