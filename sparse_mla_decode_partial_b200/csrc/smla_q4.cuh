@@ -53,9 +53,15 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
 }
 // (scale, scale) -> (-136 scale, -136 scale); exact for a stored scale.
 __device__ __forceinline__ uint32_t q4_bias(uint32_t s2) { return bf16x2_mul(s2, 0xC308C308u); }
-// Codes in bits 0-3 and 16-19 -> their two values.
+// Codes in bits 0-3 and 16-19 -> their two values.  The and/or is one lop3
+// with both constants in registers: as two immediates it became two
+// instructions, and the integer pipe (half rate) is what decoding waits for.
 __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s2, uint32_t bias2) {
-    return bf16x2_fma((w & 0x000F000Fu) | 0x43004300u, s2, bias2);
+    uint32_t v, mask, magic;
+    asm("mov.b32 %0, 0x000F000F;" : "=r"(mask));
+    asm("mov.b32 %0, 0x43004300;" : "=r"(magic));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(mask), "r"(magic));
+    return bf16x2_fma(v, s2, bias2);
 }
 // One word -> its eight values in order.
 __device__ __forceinline__ uint4 q4_word(uint32_t w, uint32_t s2, uint32_t bias2) {
