@@ -491,10 +491,23 @@ Q4_ROW_BYTES = 416
 def _launch(name, dev, stream, *args):
     """Call an entry point with the tensors' device current, on ``stream`` or on
     that device's current stream."""
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _launch(name, dev, stream, *args)
-    _check(getattr(lib(), name)(*args, _stream(stream)), name)
+    # the stream's handle alone: building a torch.cuda.Stream costs a few
+    # microseconds, as much as the launch
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    status = getattr(lib(), name)(*args, raw)
+    if status != 0:
+        raise SmlaError(status, name)
+
+
+def _want(t, dtype, name, device, shape=None):
+    """_need() for a tensor that must be on ``device``, with the checks that pass
+    in one expression; what fails is left to _need to name."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and t.is_cuda and t.get_device() == device.index):
+        _need(t, dtype, name, device, shape)
 
 
 def _new(shape, dtype, dev, stream):
@@ -517,7 +530,7 @@ def _pages_of(cache, width, what):
 
 
 def _table(page_table, B, device):
-    _need(page_table, torch.int32, "page_table", device)
+    _want(page_table, torch.int32, "page_table", device)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, pt_stride]")
     return page_table.shape[1]
@@ -533,12 +546,12 @@ def q4_append(rows, cache, page_table, cu_rows, start, *, stream=None):
     dev = rows.device
     if rows.dim() != 2 or rows.shape[1] != D:
         raise ValueError(f"rows must be [N, {D}]")
-    _need(start, torch.int32, "start", dev)
+    _want(start, torch.int32, "start", dev)
     if start.dim() != 1:
         raise ValueError("start must be [B]")
     B = start.shape[0]
-    _need(cu_rows, torch.int32, "cu_rows", dev, (B + 1,))
-    _need(cache, torch.uint8, "cache", dev)
+    _want(cu_rows, torch.int32, "cu_rows", dev, (B + 1,))
+    _want(cache, torch.uint8, "cache", dev)
     num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
     pt_stride = _table(page_table, B, dev)
     _launch("smla_q4_append", dev, stream, _ptr(rows), _k_in_range(rows.shape[0]), _ptr(cu_rows),
@@ -552,14 +565,14 @@ def q4_read(cache, page_table, positions, *, out=None, stream=None):
     _need(cache, torch.uint8, "cache")
     dev = cache.device
     num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
-    _need(positions, torch.int32, "positions", dev)
+    _want(positions, torch.int32, "positions", dev)
     if positions.dim() != 2:
         raise ValueError("positions must be [B, K]")
     B, K = positions.shape
     pt_stride = _table(page_table, B, dev)
     if out is None:
         out = _new((B, K, D), torch.bfloat16, dev, stream)
-    _need(out, torch.bfloat16, "out", dev, (B, K, D))
+    _want(out, torch.bfloat16, "out", dev, (B, K, D))
     _launch("smla_q4_read", dev, stream, _ptr(cache), num_pages, _ptr(page_table), pt_stride,
             _ptr(positions), B, _k_in_range(K), PAGE_SIZE, _ptr(out))
     return out
@@ -583,7 +596,7 @@ def _q4_decode_args(q, cache, page_table):
     if q.dim() != 4 or q.shape[-1] != D:
         raise ValueError(f"q must be [B,T,H,{D}]")
     B, T, H, _ = q.shape
-    _need(cache, torch.uint8, "cache", dev)
+    _want(cache, torch.uint8, "cache", dev)
     return dev, B, T, H, _pages_of(cache, Q4_ROW_BYTES, "cache"), _table(page_table, B, dev)
 
 
@@ -592,15 +605,15 @@ def _decode_out(dev, B, T, H, need, workspace, o, lse, stream):
     if workspace is None:
         workspace = _new(max(need, 16), torch.uint8, dev, stream)
     else:
-        _need(workspace, torch.uint8, "workspace", dev)
+        _want(workspace, torch.uint8, "workspace", dev)
     if o is None:
         o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
     else:
-        _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
+        _want(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     if lse is None:
         lse = _new((B, T, H), torch.float32, dev, stream)
     else:
-        _need(lse, torch.float32, "lse", dev, (B, T, H))
+        _want(lse, torch.float32, "lse", dev, (B, T, H))
     return workspace, o, lse
 
 
@@ -609,7 +622,7 @@ def decode_q4(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, works
     """decode() over a 4-bit cache (uint8 [num_pages, 64, 416], as q4_append
     writes it); returns (o bf16 [B,T,H,512], lse fp32 [B,T,H])."""
     dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
-    _need(idx, torch.int32, "idx", dev)
+    _want(idx, torch.int32, "idx", dev)
     if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, T):
         raise ValueError("idx must be [B,T,K]")
     K = _k_in_range(idx.shape[2])
@@ -629,7 +642,7 @@ def decode_dense_q4(q, cache, page_table, seq_lens, scale: float, nsplit: int = 
     positions 0 .. seq_lens[b, t] - 1 of sequence b.  K defaults to the longest
     length (read from seq_lens, which synchronises)."""
     dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
+    _want(seq_lens, torch.int32, "seq_lens", dev)
     if tuple(seq_lens.shape) != (B, T):
         raise ValueError("seq_lens must be [B,T]")
     if K is None:
@@ -674,12 +687,12 @@ def evict_accumulate(q, cache, page_table, seq_lens, lse, scale: float, acc, *, 
         raise ValueError(f"q must be [B,T,H,{D}]")
     B, T, H, _ = q.shape
     q4 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
-    _need(cache, torch.uint8 if q4 else torch.bfloat16, "cache", dev)
+    _want(cache, torch.uint8 if q4 else torch.bfloat16, "cache", dev)
     num_pages = _pages_of(cache, Q4_ROW_BYTES if q4 else D, "cache")
     pt_stride = _table(page_table, B, dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev, (B, T))
-    _need(lse, torch.float32, "lse", dev, (B, T, H))
-    _need(acc, torch.float32, "acc", dev)
+    _want(seq_lens, torch.int32, "seq_lens", dev, (B, T))
+    _want(lse, torch.float32, "lse", dev, (B, T, H))
+    _want(acc, torch.float32, "acc", dev)
     if acc.dim() != 2 or acc.shape[0] != B:
         raise ValueError("acc must be [B, max_n]")
     _launch("smla_evict_accumulate_q4" if q4 else "smla_evict_accumulate", dev, stream, _ptr(q),
@@ -703,9 +716,9 @@ def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, 
     K = _k_in_range(int(K))
     if K < 1:
         raise ValueError("K must be at least 1")
-    _need(n, torch.int32, "n", dev, (B,))
+    _want(n, torch.int32, "n", dev, (B,))
     if pos is not None:
-        _need(pos, torch.int32, "pos", dev, (B, max_n))
+        _want(pos, torch.int32, "pos", dev, (B, max_n))
     outs = []
     for t, name, dtype, shape in ((src, "src", torch.int32, (B, K)), (n_new, "n_new", torch.int32, (B,)),
                                   (acc_new, "acc_new", torch.float32, (B, max_n)),
@@ -713,13 +726,13 @@ def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, 
         if t is None:
             t = _new(shape, dtype, dev, stream)
         else:
-            _need(t, dtype, name, dev, shape)
+            _want(t, dtype, name, dev, shape)
         outs.append(t)
     src, n_new, acc_new, pos_new = outs
     if workspace is None:
         workspace = _new(max(16, evict_workspace_bytes(B, max_n)), torch.uint8, dev, stream)
     else:
-        _need(workspace, torch.uint8, "workspace", dev)
+        _want(workspace, torch.uint8, "workspace", dev)
     _launch("smla_evict_plan", dev, stream, _ptr(acc), _ptr(pos), _ptr(n), B, max_n, K, int(n_sink),
             int(n_recent), _ptr(workspace), workspace.numel(), _ptr(src), _ptr(n_new),
             _ptr(acc_new), _ptr(pos_new))
