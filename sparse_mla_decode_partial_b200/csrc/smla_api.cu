@@ -1449,6 +1449,14 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
+// CTAs per sequence of the plan: as many as keep the whole batch in one wave,
+// while each still has a thread per slot.
+int plan_cluster(int B, int max_n, int sms) {
+    int nc = 1;
+    while (nc < smla::kPlanMaxCluster && 2ll * nc * B <= sms && 2ll * nc * smla::kPlanThreads <= max_n) nc *= 2;
+    return nc;
+}
+
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a != nullptr && b != nullptr && x < y + nb && y < x + na;
@@ -1486,6 +1494,7 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
     if ((long long)n_sink + n_recent > K) return SMLA_ERR_INVALID_ARG;
     if (max_n > SMLA_EVICT_MAX_N || K > SMLA_MAX_K) return SMLA_ERR_UNSUPPORTED;
     if (B == 0) return SMLA_OK;
+    if (B > INT_MAX / smla::kPlanMaxCluster) return SMLA_ERR_INVALID_ARG;
     if (!n || !src || !n_new || (max_n > 0 && !acc)) return SMLA_ERR_INVALID_ARG;
     if (!aligned(acc, 4) || !aligned(pos, 4) || !aligned(n, 4) || !aligned(src, 4) || !aligned(n_new, 4) ||
         !aligned(acc_new, 4) || !aligned(pos_new, 4))
@@ -1511,13 +1520,23 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
     p.n_new = n_new;
     p.acc_new = acc_new;
     p.pos_new = pos_new;
-    int smem = smla::plan_fixed_bytes(max_n);
-    p.cached = smem + 4ll * max_n <= kMaxSmemBytes;
-    if (p.cached) smem += 4 * max_n;
+    const int nc = plan_cluster(B, max_n, current_device_sms());
+    p.per = (int)(((long long)max_n + nc - 1) / nc + 31) / 32 * 32;
+    int smem = smla::plan_fixed_bytes(p.per);
+    p.cached = smem + 4ll * p.per <= kMaxSmemBytes;
+    if (p.cached) smem += 4 * p.per;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_evict_plan_kernel), kMaxSmemBytes);
     if (e != cudaSuccess) return cuda_fail(e);
-    e = launch_dependent(smla::smla_evict_plan_kernel, B, smla::kPlanThreads, (size_t)smem,
-                         static_cast<cudaStream_t>(stream), p);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pdl_config(static_cast<cudaStream_t>(stream), attr);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)nc;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(B * nc));
+    cfg.blockDim = dim3(smla::kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    e = cudaLaunchKernelEx(&cfg, smla::smla_evict_plan_kernel, p);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
@@ -1536,7 +1555,8 @@ smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *pa
         if (row_bytes[k] < 1 || row_bytes[k] > SMLA_EVICT_MAX_ROW_BYTES) return SMLA_ERR_UNSUPPORTED;
         if (row_bytes[k] % 16) return SMLA_ERR_MISALIGNED;
         p.buf[k] = static_cast<uint8_t *>(caches[k]);
-        p.row_bytes[k] = row_bytes[k];
+        p.pieces[k] = row_bytes[k] / 16;
+        p.total += row_bytes[k] / 16;
     }
     p.src = src;
     p.B = B;

@@ -238,112 +238,195 @@ struct EvictPlanParams {
     int *n_new;          // [B]
     float *acc_new;      // [B, max_n] or null
     int *pos_new;        // [B, max_n] or null
-    int cached;          // keys fit in shared memory
+    int per;             // slots of a CTA: a multiple of 32
+    int cached;          // their keys fit in shared memory
 };
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 2048;
-__host__ __device__ constexpr int plan_words(int max_n) { return (max_n + 31) / 32; }
-// histogram, scan scratch, two bitmaps and word prefixes, then the keys
-__host__ __device__ constexpr int plan_fixed_bytes(int max_n) {
-    return kPlanBins * 4 + 256 + 3 * 4 * plan_words(max_n);
+constexpr int kPlanMaxCluster = 8;
+// a histogram and two of sums, scan scratch and exchanged counts, two bitmaps and word
+// prefixes, then (cached) the keys
+__host__ __device__ constexpr int plan_fixed_bytes(int per) {
+    return 3 * kPlanBins * 4 + 512 + 3 * 4 * (per / 32);
 }
 
-// Key of a slot: larger stays.  Protected slots above every weight; NaN counts
-// as -inf; -0 equals +0.
-__device__ __forceinline__ uint32_t evict_key(const EvictPlanParams &p, size_t base, int i, long long recent) {
-    const int pos = p.pos != nullptr ? ld_input(p.pos + base + i) : i;
-    if (pos < p.n_sink || (long long)pos >= recent) return 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Barrier of the cluster; orders shared and global memory among its threads.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of shared memory at `p`'s place in CTA `rank` of the cluster.
+__device__ __forceinline__ unsigned ld_cluster(const void *p, uint32_t rank) {
+    uint32_t a;
+    unsigned v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void add_cluster(const void *p, unsigned v, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Order-preserving key of a weight: larger stays; NaN counts as -inf, -0 as +0.
+__device__ __forceinline__ uint32_t evict_key(float a) { return a != a ? 0x007FFFFFu : ix_key(a); }
+__device__ __forceinline__ float ld_weight(const float *p) {
     float a;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(a) : "l"(p.acc + base + i));
-    return a != a ? 0x007FFFFFu : ix_key(a);
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(a) : "l"(p));
+    return a;
 }
 
-// One CTA per sequence: radix selection of the K-th largest key (digits of 11,
-// 11 and 10 bits), bitmaps of the slots above and at it, ties to the smaller
-// slot, then ranks of holes and movers by prefix sums over the bitmaps' words.
+// One cluster of CTAs per sequence, each CTA a run of its slots: radix
+// selection of the K-th largest key (digits of 11, 11 and 10 bits, counts
+// summed in the first CTA), bitmaps of the slots above and at it, ties to the
+// smaller slot, then ranks of holes and movers by prefix sums.  A handful of
+// block and cluster barriers with little work between them: latency bounds it.
 __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const EvictPlanParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int words = plan_words(p.max_n);
+    const int words = p.per / 32;
     unsigned *hist = reinterpret_cast<unsigned *>(smem);
-    int *scratch = reinterpret_cast<int *>(smem + kPlanBins * 4);  // 33 ints, then dec[4] at 40
-    int *dec = scratch + 40;
-    uint32_t *keep = reinterpret_cast<uint32_t *>(scratch + 64);
+    unsigned *sum2 = hist + kPlanBins;                                 // the cluster's counts (first CTA)
+    int *scratch = reinterpret_cast<int *>(smem + 3 * kPlanBins * 4);  // 33 ints
+    int *dec = scratch + 40;   // 4 ints
+    int *xch = scratch + 48;   // counts that the cluster exchanges
+    uint32_t *keep = reinterpret_cast<uint32_t *>(scratch + 128);
     uint32_t *tie = keep + words;
     int *pre = reinterpret_cast<int *>(tie + words);
     uint32_t *keys = reinterpret_cast<uint32_t *>(pre + words);
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t nc = cluster_size(), rank = cluster_rank();
+    const int b = blockIdx.x / nc, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const size_t base = (size_t)b * p.max_n;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int raw = ld_input(p.n + b);
     const int n = min(max(raw, 0), p.max_n);
-    if (tid == 0 && raw != n) count_bad_index();
+    if (tid == 0 && rank == 0 && raw != n) count_bad_index();
     const int m = min(n, p.K);
-    if (tid == 0) p.n_new[b] = m;
+    if (tid == 0 && rank == 0) p.n_new[b] = m;
     int *src = p.src + (size_t)b * p.K;
-    if (n > p.K) {
+    const int lo = (int)rank * p.per, hi = min(n, lo + p.per);  // this CTA's slots
+    const bool cut = n > p.K;                                  // the same in the whole cluster
+    if (cut) {
+        for (int i = tid; i < 3 * kPlanBins; i += kPlanThreads) hist[i] = 0u;
+        // weights in, and the newest position
+        int top = INT_MIN;
+#pragma unroll 4
+        for (int i = lo + tid; i < hi; i += kPlanThreads) {
+            if (p.pos != nullptr) top = max(top, ld_input(p.pos + base + i));
+            if (p.cached) keys[i - lo] = evict_key(ld_weight(p.acc + base + i));
+        }
         long long end = n;
         if (p.pos != nullptr) {
-            int top = INT_MIN;
-            for (int i = tid; i < n; i += kPlanThreads) top = max(top, ld_input(p.pos + base + i));
             top = __reduce_max_sync(0xffffffffu, top);
             if (lane == 0) scratch[warp] = top;
             __syncthreads();
-            top = scratch[lane];
-            end = (long long)__reduce_max_sync(0xffffffffu, top) + 1;
-            __syncthreads();
+            if (warp == 0) {
+                top = __reduce_max_sync(0xffffffffu, scratch[lane]);
+                if (lane == 0) xch[0] = top;
+            }
+            cluster_sync();
+            top = INT_MIN;
+            for (uint32_t r = 0; r < nc; ++r) top = max(top, (int)ld_cluster(&xch[0], r));
+            end = (long long)top + 1;
         }
         const long long recent = end - p.n_recent;
-        if (p.cached)
-            for (int i = tid; i < n; i += kPlanThreads) keys[i] = evict_key(p, base, i, recent);
-        auto key_of = [&](int i) { return p.cached ? keys[i] : evict_key(p, base, i, recent); };
+        auto safe = [&](int i) {
+            const int pos = p.pos != nullptr ? ld_input(p.pos + base + i) : i;
+            return pos < p.n_sink || (long long)pos >= recent;
+        };
+        auto key_of = [&](int i) {
+            if (p.cached) return keys[i - lo];
+            return safe(i) ? 0xFFFFFFFFu : evict_key(ld_weight(p.acc + base + i));
+        };
+        if (p.cached && (p.n_sink > 0 || p.n_recent > 0)) {
+#pragma unroll 4
+            for (int i = lo + tid; i < hi; i += kPlanThreads)
+                if (safe(i)) keys[i - lo] = 0xFFFFFFFFu;
+        }
+        cluster_sync();  // the cleared sums too
 
         uint32_t prefix = 0;  // the K-th largest key, digit by digit
         int need = p.K;
+#pragma unroll 1
         for (int digit = 0; digit < 3; ++digit) {
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
             const int bits = digit == 2 ? 10 : 11;
-            for (int i = tid; i < kPlanBins; i += kPlanThreads) hist[i] = 0u;
-            __syncthreads();
-            for (int i = tid; i < n; i += kPlanThreads) {
+            for (int i = lo + tid; i < hi; i += kPlanThreads) {
                 const uint32_t k = key_of(i);
                 if (digit == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
                     atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
             }
             __syncthreads();
-            // thread t holds bins 2047 - 2 t and 2046 - 2 t: counts from the top
-            const unsigned h1 = hist[kPlanBins - 1 - 2 * tid], h0 = hist[kPlanBins - 2 - 2 * tid];
-            int total;
-            const int incl = ix_block_scan((int)(h1 + h0), scratch, &total);
-            const int excl = incl - (int)(h1 + h0);
-            if (excl < need && need <= incl) {
-                const bool first = excl + (int)h1 >= need;
-                dec[0] = kPlanBins - (first ? 1 : 2) - 2 * tid;
-                dec[1] = need - excl - (first ? 0 : (int)h1);
+            // The first CTA sums the counts and finds the bucket.  Only bins
+            // that hold something travel (a few dozen): every CTA reading every
+            // other's histogram took 6 us a digit.  Sums alternate between two
+            // arrays, so that the next digit's never meet these.
+            unsigned *sum = sum2 + (digit & 1) * kPlanBins;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const unsigned v = hist[tid + k * kPlanThreads];
+                if (v) {
+                    hist[tid + k * kPlanThreads] = 0u;
+                    add_cluster(&sum[tid + k * kPlanThreads], v, 0);
+                }
             }
-            __syncthreads();
-            prefix |= (uint32_t)dec[0] << shift;
-            need = dec[1];
-            __syncthreads();
+            cluster_sync();
+            if (rank == 0) {
+                // thread t holds bins 2047 - 2 t and 2046 - 2 t: counts from the top
+                const unsigned h1 = sum[kPlanBins - 1 - 2 * tid], h0 = sum[kPlanBins - 2 - 2 * tid];
+                sum2[((digit & 1) ^ 1) * kPlanBins + tid] = 0u;
+                sum2[((digit & 1) ^ 1) * kPlanBins + tid + kPlanThreads] = 0u;
+                int total;
+                const int incl = ix_block_scan((int)(h1 + h0), scratch, &total);
+                const int excl = incl - (int)(h1 + h0);
+                if (excl < need && need <= incl) {
+                    const bool first = excl + (int)h1 >= need;
+                    dec[0] = kPlanBins - (first ? 1 : 2) - 2 * tid;
+                    dec[1] = need - excl - (first ? 0 : (int)h1);
+                }
+            }
+            cluster_sync();
+            prefix |= ld_cluster(&dec[0], 0) << shift;
+            need = (int)ld_cluster(&dec[1], 0);
         }
 
         // bitmaps: slots above the K-th key, slots equal to it
-        const int nw = (n + 31) / 32;
+        const int nw = hi > lo ? (hi - lo + 31) / 32 : 0;
+        int equal_here = 0;
         for (int w = warp; w < nw; w += kPlanThreads / 32) {
-            const int i = 32 * w + lane;
-            const uint32_t k = i < n ? key_of(i) : 0u;
-            const uint32_t above = __ballot_sync(0xffffffffu, i < n && k > prefix);
-            const uint32_t equal = __ballot_sync(0xffffffffu, i < n && k == prefix);
+            const int i = lo + 32 * w + lane;
+            const uint32_t k = i < hi ? key_of(i) : 0u;
+            const uint32_t above = __ballot_sync(0xffffffffu, i < hi && k > prefix);
+            const uint32_t equal = __ballot_sync(0xffffffffu, i < hi && k == prefix);
             if (lane == 0) {
                 keep[w] = above;
                 tie[w] = equal;
+                equal_here += __popc(equal);
             }
         }
+        if (lane == 0) scratch[warp] = equal_here;
         __syncthreads();
+        if (warp == 0) {
+            const int x = __reduce_add_sync(0xffffffffu, scratch[lane]);
+            if (lane == 0) xch[1] = x;
+        }
+        cluster_sync();
         // the first `need` ties stay
         int carry = 0;
+        for (uint32_t r = 0; r < rank; ++r) carry += (int)ld_cluster(&xch[1], r);
         for (int w0 = 0; w0 < nw; w0 += kPlanThreads) {
             const int w = w0 + tid;
             const uint32_t t = w < nw ? tie[w] : 0u;
@@ -361,50 +444,70 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
             carry += total;
         }
         __syncthreads();
-        // movers: slots at or behind m that stay, in order
-        auto below = [&](int w) { return 32 * w + 32 <= m ? 0xffffffffu : 32 * w >= m ? 0u : (1u << (m - 32 * w)) - 1u; };
-        carry = 0;
+        // movers (slots at or behind m that stay) and holes (slots before m
+        // that leave): a slot run lies on both sides of m in one word at most
+        auto below = [&](int w) {
+            const int s0 = lo + 32 * w;
+            return s0 + 32 <= m ? 0xffffffffu : s0 >= m ? 0u : (1u << (m - s0)) - 1u;
+        };
+        int mv_here = 0, hole_here = 0;
+        for (int w = tid; w < nw; w += kPlanThreads) {
+            mv_here += __popc(keep[w] & ~below(w));
+            hole_here += __popc(~keep[w] & below(w));
+        }
+        mv_here = __reduce_add_sync(0xffffffffu, mv_here);
+        hole_here = __reduce_add_sync(0xffffffffu, hole_here);
+        if (tid == 0) xch[2] = xch[3] = 0;
+        __syncthreads();
+        if (lane == 0 && (mv_here | hole_here)) {
+            atomicAdd(&xch[2], mv_here);
+            atomicAdd(&xch[3], hole_here);
+        }
+        cluster_sync();
+        int mv = 0, hole = 0;
+        for (uint32_t r = 0; r < rank; ++r) {
+            mv += (int)ld_cluster(&xch[2], r);
+            hole += (int)ld_cluster(&xch[3], r);
+        }
         for (int w0 = 0; w0 < nw; w0 += kPlanThreads) {
             const int w = w0 + tid;
-            const uint32_t mv = w < nw ? keep[w] & ~below(w) : 0u;
+            const uint32_t mvs = w < nw ? keep[w] & ~below(w) : 0u, holes = w < nw ? ~keep[w] & below(w) : 0u;
             int total;
-            const int incl = ix_block_scan(__popc(mv), scratch, &total);
-            int at = carry + incl - __popc(mv);
-            for (uint32_t left = mv; left; left &= left - 1u) p.movers[base + at++] = 32 * w + __ffs(left) - 1;
-            carry += total;
+            const int mine = __popc(mvs);
+            const int at_mv = ix_block_scan(mine, scratch, &total) - mine;
+            int x = mv + at_mv;
+            for (uint32_t left = mvs; left; left &= left - 1u) p.movers[base + x++] = lo + 32 * w + __ffs(left) - 1;
+            mv += total;
+            const int gone = __popc(holes);
+            const int at_hole = ix_block_scan(gone, scratch, &total) - gone;
+            if (w < nw) pre[w] = hole + at_hole;
+            hole += total;
         }
-        // holes before each word
-        carry = 0;
-        for (int w0 = 0; w0 < nw; w0 += kPlanThreads) {
-            const int w = w0 + tid;
-            const uint32_t hole = w < nw ? ~keep[w] & below(w) : 0u;
-            int total;
-            const int incl = ix_block_scan(__popc(hole), scratch, &total);
-            if (w < nw) pre[w] = carry + incl - __popc(hole);
-            carry += total;
-        }
-        __syncthreads();  // the movers' list and pre are complete (one CTA wrote both)
+        cluster_sync();  // the movers' list and pre are complete; no CTA leaves while another reads its counts
     }
-    for (int i = tid; i < max(p.K, p.max_n); i += kPlanThreads) {
-        int s = -1;
-        if (i < m) {
-            s = i;
-            if (n > p.K && !((keep[i >> 5] >> (i & 31)) & 1u)) {
-                const uint32_t lower = (1u << (i & 31)) - 1u;
-                s = ld_input(p.movers + base + pre[i >> 5] + __popc(~keep[i >> 5] & lower));
-            }
-        }
+    // this CTA's slots, then its share of what lies behind n
+    auto put = [&](int i, int s) {
         if (i < p.K) src[i] = s;
         if (i < p.max_n) {
-            if (p.acc_new != nullptr) {
-                float a = 0.f;
-                if (s >= 0) asm volatile("ld.global.f32 %0, [%1];" : "=f"(a) : "l"(p.acc + base + s));
-                p.acc_new[base + i] = a;
-            }
+            if (p.acc_new != nullptr) p.acc_new[base + i] = s < 0 ? 0.f : ld_weight(p.acc + base + s);
             if (p.pos_new != nullptr)
                 p.pos_new[base + i] = s < 0 ? -1 : p.pos != nullptr ? ld_input(p.pos + base + s) : s;
         }
+    };
+#pragma unroll 4
+    for (int i = lo + tid; i < hi; i += kPlanThreads) {
+        int s = i < m ? i : -1;
+        if (cut && i < m) {
+            const uint32_t k = keep[(i - lo) >> 5];
+            if (!((k >> ((i - lo) & 31)) & 1u)) {
+                const uint32_t lower = (1u << ((i - lo) & 31)) - 1u;
+                s = ld_input(p.movers + base + pre[(i - lo) >> 5] + __popc(~k & lower));
+            }
+        }
+        put(i, s);
     }
+    for (long long i = n + (long long)rank * kPlanThreads + tid; i < max(p.K, p.max_n); i += nc * kPlanThreads)
+        put((int)i, -1);
 }
 
 // ---------------------------------------------------------------- apply
@@ -419,38 +522,68 @@ struct EvictApplyParams {
     int pt_stride;
     long long num_pages;
     uint8_t *buf[kEvictBuffers];
-    int row_bytes[kEvictBuffers];  // multiples of 16
+    int pieces[kEvictBuffers];  // 16-byte pieces of a row
     int n_buf;
+    int total;                  // pieces of a row over all buffers
 };
 constexpr int kApplyWarps = 8;
+constexpr int kApplyDepth = 8;  // pieces in flight per lane
 
-// One warp per 32 list entries; it copies the moved rows one after the other.
+// One warp per 32 list entries.  It lists the moves among them, then its lanes
+// walk the moves' 16-byte pieces, all buffers in a row, eight loads in flight
+// each before the first store.  Bound by memory.
 __global__ void __launch_bounds__(32 * kApplyWarps) smla_evict_apply_kernel(const EvictApplyParams p) {
+    __shared__ int from_s[kApplyWarps][32], to_s[kApplyWarps][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long per = (p.K + 31) / 32;
-    const long long unit = (long long)blockIdx.x * kApplyWarps + (threadIdx.x >> 5);
+    const long long unit = (long long)blockIdx.x * kApplyWarps + warp;
     if (unit >= per * p.B) return;
     const int b = (int)(unit / per), i = (int)(unit % per) * 32 + lane;
     const int s = i < p.K ? ld_input(p.src + (size_t)b * p.K + i) : -1;
-    const bool moves = s != -1 && s != i;
-    long long from = -1, to = -1;
-    if (moves) {
+    long long from = -1, to = -1;  // rows of the pool: below 2^31
+    if (s != -1 && s != i) {
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
         from = paged_row(pt_b, p.pt_stride, p.num_pages, s);
         to = paged_row(pt_b, p.pt_stride, p.num_pages, i);
         if (from < 0 || to < 0) count_bad_index();
     }
-    for (uint32_t todo = __ballot_sync(0xffffffffu, from >= 0 && to >= 0); todo; todo &= todo - 1u) {
-        const int l = __ffs(todo) - 1;
-        const long long f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, to, l);
-        for (int k = 0; k < p.n_buf; ++k) {
-            const uint8_t *in = p.buf[k] + f * p.row_bytes[k];
-            uint8_t *out = p.buf[k] + t * p.row_bytes[k];
-            for (int x = 16 * lane; x < p.row_bytes[k]; x += 512)
-                *reinterpret_cast<uint4 *>(out + x) = ld_row16(in + x);
+    const uint32_t moves = __ballot_sync(0xffffffffu, from >= 0 && to >= 0);
+    if ((moves >> lane) & 1u) {
+        const int k = __popc(moves & ((1u << lane) - 1u));
+        from_s[warp][k] = (int)from;
+        to_s[warp][k] = (int)to;
+    }
+    __syncwarp();
+    const int n = __popc(moves);
+    int move = 0, piece = lane;
+    while (piece >= p.total) {
+        piece -= p.total;
+        ++move;
+    }
+    while (__any_sync(0xffffffffu, move < n)) {
+        uint4 v[kApplyDepth];
+        uint8_t *dst[kApplyDepth];
+#pragma unroll
+        for (int k = 0; k < kApplyDepth; ++k) {
+            dst[k] = nullptr;
+            if (move < n) {
+                int x = piece, q = 0;
+                while (x >= p.pieces[q]) x -= p.pieces[q++];
+                const size_t row = (size_t)p.pieces[q] * 16;
+                dst[k] = p.buf[q] + to_s[warp][move] * row + 16 * x;
+                v[k] = ld_row16(p.buf[q] + from_s[warp][move] * row + 16 * x);
+                piece += 32;
+                while (piece >= p.total) {
+                    piece -= p.total;
+                    ++move;
+                }
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kApplyDepth; ++k)
+            if (dst[k] != nullptr) *reinterpret_cast<uint4 *>(dst[k]) = v[k];
     }
 }
 

@@ -147,6 +147,17 @@ def test_plan_sizes(most, n, K):
     run_plan(rng.exponential(1.0, (len(n), most)), n, K)
 
 
+@pytest.mark.parametrize("B,most,K", [(1, 8192, 8000), (2, 16385, 9000), (20, 9000, 8999), (40, 4100, 1000), (80, 2500, 2400),
+                                      (1, 460001, 300000)])
+def test_plan_batches_and_lengths_over_the_cluster_sizes(B, most, K):
+    """Sequences shared by one to eight thread blocks, with positions, ragged, and
+    too long for the keys to be kept in shared memory."""
+    rng = np.random.default_rng(B)
+    n = [most] + [int(x) for x in rng.integers(0, most + 1, B - 1)]
+    pos = np.stack([rng.permutation(most) for _ in range(B)]).astype(np.int32)
+    run_plan(np.round(rng.exponential(1.0, (B, most)), 3), n, K, pos=pos, n_sink=5, n_recent=100)
+
+
 @pytest.mark.parametrize("kind", ["equal", "few", "zeros", "negative", "special"])
 def test_plan_ties_and_special_weights(kind):
     rng = np.random.default_rng(1)
