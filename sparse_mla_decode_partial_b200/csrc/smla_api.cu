@@ -1565,7 +1565,7 @@ smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *pa
     p.pt_stride = pt_stride;
     p.num_pages = num_pages;
     p.n_buf = n_caches;
-    const long long units = (long long)B * ((K + 31ll) / 32);
+    const long long units = (long long)B * ((K + smla::kApplySlots - 1ll) / smla::kApplySlots);
     const long long blocks = (units + smla::kApplyWarps - 1) / smla::kApplyWarps;
     if (blocks > INT_MAX) return SMLA_ERR_INVALID_ARG;
     const cudaError_t e = launch_dependent(smla::smla_evict_apply_kernel, (int)blocks, 32 * smla::kApplyWarps, 0,

@@ -87,7 +87,7 @@ __device__ __forceinline__ void weigh_scores(const uint8_t *row0, const uint4 *f
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 d[n] = ld_row16(mine + n * 8 * kRow + 16 * (4 * j + c));
-                s2[n] = ld_scale2(mine + n * 8 * kRow + kQ4OffScale + 2 * (4 * j + c));
+                s2[n] = ld_scale(mine + n * 8 * kRow + kQ4OffScale + 2 * (4 * j + c));
             }
         };
         load(0, code, sc);
@@ -105,7 +105,8 @@ __device__ __forceinline__ void weigh_scores(const uint8_t *row0, const uint4 *f
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const uint32_t word = w == 0 ? code[n].x : w == 1 ? code[n].y : w == 2 ? code[n].z : code[n].w;
-                    v[n] = q4_word(word, sc[n], q4_bias(sc[n]));
+                    const uint32_t s2 = q4_scale2(sc[n]);
+                    v[n] = q4_word(word, s2, q4_bias(s2));
                 }
                 chunk(8 * j + 2 * w, v);
             }
@@ -528,20 +529,21 @@ struct EvictApplyParams {
 };
 constexpr int kApplyWarps = 8;
 constexpr int kApplyDepth = 8;  // pieces in flight per lane
+constexpr int kApplySlots = 16; // list entries per warp
 
-// One warp per 32 list entries.  It lists the moves among them, then its lanes
+// One warp per kApplySlots list entries.  It lists the moves among them, then its lanes
 // walk the moves' 16-byte pieces, all buffers in a row, eight loads in flight
 // each before the first store.  Bound by memory.
 __global__ void __launch_bounds__(32 * kApplyWarps) smla_evict_apply_kernel(const EvictApplyParams p) {
-    __shared__ int from_s[kApplyWarps][32], to_s[kApplyWarps][32];
+    __shared__ int from_s[kApplyWarps][kApplySlots], to_s[kApplyWarps][kApplySlots];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long per = (p.K + 31) / 32;
+    const long long per = (p.K + kApplySlots - 1) / kApplySlots;
     const long long unit = (long long)blockIdx.x * kApplyWarps + warp;
     if (unit >= per * p.B) return;
-    const int b = (int)(unit / per), i = (int)(unit % per) * 32 + lane;
-    const int s = i < p.K ? ld_input(p.src + (size_t)b * p.K + i) : -1;
+    const int b = (int)(unit / per), i = (int)(unit % per) * kApplySlots + lane;
+    const int s = lane < kApplySlots && i < p.K ? ld_input(p.src + (size_t)b * p.K + i) : -1;
     long long from = -1, to = -1;  // rows of the pool: below 2^31
     if (s != -1 && s != i) {
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;

@@ -112,14 +112,15 @@ static_assert(TcCfg::kSmemBytes <= 232448, "shared memory per CTA");
 static_assert(32 * TcCfgT<true>::kProducerWarps * 2 == 32 * kQ4Groups + 32 * 8, "two units per producer thread");
 
 // What one producer thread holds of a tile of 4-bit rows: two of its 768
-// units.  Unit u < 512 is group (u / 8) % 16 of row u % 8 + 8 (u / 128): eight
-// lanes write the same group of eight rows, whose swizzled 16-byte chunks fall
-// in distinct banks, and a warp reads 64 bytes of each row.  The others are
-// 16-byte pieces of rope values, v = u - 512: piece (v / 8) % 8 of row v % 8 +
-// 8 (v / 64).
+// units.  Unit u < 512 is group u % 16 of row u / 16, so that a warp reads the
+// codes and scales of two rows whole; lanes store their group's four 16-byte
+// chunks in rotated order, which puts the eight of a store phase in distinct
+// banks.  The others are 16-byte pieces of rope values, v = u - 512: piece v % 8
+// of row v / 8.
+constexpr int kQ4Ahead = 3;
 struct Q4Units {
     uint4 d[2];
-    uint32_t s2[2];  // the group's scale, twice
+    uint32_t scale[2];
 };
 
 template <bool DIRECT, bool Q4 = false>
@@ -273,10 +274,9 @@ __global__ void __launch_bounds__(TcCfgT<Q4>::kThreads, 1)
             named_bar_sync(bar_prod, 32 * C::kProducerWarps);  // rows_s complete
             const int chunk_tiles = (n + C::kTileRows - 1) / C::kTileRows;
             if constexpr (Q4) {
-                // Two units per thread and tile; the next tile's loads are in
-                // flight while this one is decoded.
+                // two units per thread and tile
                 auto unit_row = [&](int t, int u) {
-                    const int r = u < 512 ? (u & 7) + 8 * (u >> 7) : (u & 7) + 8 * ((u - 512) >> 6);
+                    const int r = u < 512 ? u >> 4 : (u - 512) >> 3;
                     const int j = t * C::kTileRows + r;
                     return j < n ? rows_s[j] : -1;
                 };
@@ -286,55 +286,71 @@ __global__ void __launch_bounds__(TcCfgT<Q4>::kThreads, 1)
                         const int u = ptid + k * kPT;
                         const int row = unit_row(t, u);
                         x.d[k] = make_uint4(0u, 0u, 0u, 0u);
-                        x.s2[k] = 0u;  // a padding slot decodes to zeros
+                        x.scale[k] = 0u;  // a padding slot decodes to zeros
                         if (row < 0) continue;
                         const uint8_t *src = cache + (size_t)row * kQ4RowBytes;
                         if (u < 512) {
-                            const int g = (u >> 3) & 15;
+                            const int g = u & 15;
                             x.d[k] = ld_row16(src + 16 * g);
-                            x.s2[k] = ld_scale2(src + kQ4OffScale + 2 * g);
+                            x.scale[k] = ld_scale(src + kQ4OffScale + 2 * g);
                         } else {
-                            x.d[k] = ld_row16(src + kQ4OffRope + 16 * ((u >> 3) & 7));
+                            x.d[k] = ld_row16(src + kQ4OffRope + 16 * (u & 7));
                         }
                     }
                 };
-                Q4Units cur, next;
-                load(0, cur);
-                for (int t = 0; t < chunk_tiles; ++t, ++it) {
-                    const int stage = it % C::kStages;
-                    if (t + 1 < chunk_tiles) load(t + 1, next);
-                    if (it >= C::kStages) mbar_wait(&kv_empty[stage], ((it / C::kStages) - 1) & 1, dead);
-                    uint8_t *dst = smem + C::kOffKV + C::tile_off(stage);
+                // kQ4Ahead tiles of loads in flight per thread: with one ahead a
+                // tile of random rows took a memory latency
+                Q4Units buf[kQ4Ahead];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int u = ptid + k * kPT;
-                        if (u < 512) {
-                            const int r = (u & 7) + 8 * (u >> 7), g = (u >> 3) & 15;
-                            uint8_t *line = dst + (g >> 1) * C::kBoxStride + r * 128;
-                            const uint32_t bias = q4_bias(cur.s2[k]);
-                            const uint32_t w[4] = {cur.d[k].x, cur.d[k].y, cur.d[k].z, cur.d[k].w};
+                for (int k = 0; k < kQ4Ahead; ++k)
+                    if (k < chunk_tiles) load(k, buf[k]);
+                for (int t0 = 0; t0 < chunk_tiles; t0 += kQ4Ahead) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4 *>(line + (((4 * (g & 1) + i) ^ (r & 7)) << 4)) =
-                                    q4_word(w[i], cur.s2[k], bias);
-                        } else {
-                            const int r = (u & 7) + 8 * ((u - 512) >> 6), ch = (u >> 3) & 7;
-                            *reinterpret_cast<uint4 *>(dst + 8 * C::kBoxStride + r * 128 +
-                                                       ((ch ^ (r & 7)) << 4)) = cur.d[k];
+                    for (int a = 0; a < kQ4Ahead; ++a) {
+                        const int t = t0 + a;
+                        if (t >= chunk_tiles) break;
+                        const int stage = it % C::kStages;
+                        if (it >= C::kStages) mbar_wait(&kv_empty[stage], ((it / C::kStages) - 1) & 1, dead);
+                        uint8_t *dst = smem + C::kOffKV + C::tile_off(stage);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int u = ptid + k * kPT;
+                            if (u < 512) {
+                                const int r = u >> 4, g = u & 15, rot = (g >> 1) & 3;
+                                uint8_t *line = dst + (g >> 1) * C::kBoxStride + r * 128;
+                                const uint32_t s2 = q4_scale2(buf[a].scale[k]), bias = q4_bias(s2);
+                                const uint4 d = buf[a].d[k];
+                                const bool one = rot & 1, two = rot & 2;
+                                const uint32_t v0 = one ? d.y : d.x, v1 = one ? d.z : d.y;
+                                const uint32_t v2 = one ? d.w : d.z, v3 = one ? d.x : d.w;
+                                const uint32_t w[4] = {two ? v2 : v0, two ? v3 : v1, two ? v0 : v2, two ? v1 : v3};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<uint4 *>(
+                                        line + (((4 * (g & 1) + ((i + rot) & 3)) ^ (r & 7)) << 4)) =
+                                        q4_word(w[i], s2, bias);
+                            } else {
+                                const int r = (u - 512) >> 3, ch = u & 7;
+                                *reinterpret_cast<uint4 *>(dst + 8 * C::kBoxStride + r * 128 +
+                                                           ((ch ^ (r & 7)) << 4)) = buf[a].d[k];
+                            }
                         }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (pw == 0) {
-                        const int j = t * C::kTileRows + lane;
-                        const uint32_t vmask = __ballot_sync(0xffffffffu, j < n && rows_s[j] >= 0);
-                        if (lane == 0) {
-                            hdr[stage] = vmask;
-                            mbar_arrive(&kv_full[stage]);
+                        // (no fence.proxy.async here: it would wait for this thread's
+                        // loads in flight; the MMA issuer executes one after it has
+                        // seen the barrier, before it lets the tensor core read)
+                        __syncwarp();
+                        if (pw == 0) {
+                            const int j = t * C::kTileRows + lane;
+                            const uint32_t vmask = __ballot_sync(0xffffffffu, j < n && rows_s[j] >= 0);
+                            if (lane == 0) {
+                                hdr[stage] = vmask;
+                                mbar_arrive(&kv_full[stage]);
+                            }
                         }
+                        if (lane == 0) mbar_arrive(&kv_full[stage]);
+                        if (t + kQ4Ahead < chunk_tiles) load(t + kQ4Ahead, buf[a]);
+                        ++it;
                     }
-                    if (lane == 0) mbar_arrive(&kv_full[stage]);
-                    cur = next;
                 }
             } else
             for (int t = 0; t < chunk_tiles; ++t, ++it) {

@@ -83,12 +83,14 @@ __device__ __forceinline__ uint2 ld_row8(const uint8_t *p) {
     asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
-// A group's scale as (scale, scale).
-__device__ __forceinline__ uint32_t ld_scale2(const uint8_t *p) {
+// A group's scale, as loaded; q4_scale2 makes it (scale, scale).  Kept apart: a
+// load meant to run ahead must not be followed by arithmetic on its result.
+__device__ __forceinline__ uint32_t ld_scale(const uint8_t *p) {
     uint16_t v;
     asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return (uint32_t)v * 0x00010001u;
+    return v;
 }
+__device__ __forceinline__ uint32_t q4_scale2(uint32_t scale) { return __byte_perm(scale, scale, 0x1010); }
 
 __device__ __forceinline__ void count_bad_index() {
     atomicOr(&g_status_flags, kFlagIndexRange);
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_read_kernel(const Q4Rea
     if (row >= 0) {
         const uint8_t *src = p.cache + row * kQ4RowBytes;
         const uint2 w = ld_row8(src + 8 * lane);
-        const uint32_t s2 = ld_scale2(src + kQ4OffScale + (lane & ~1));
+        const uint32_t s2 = q4_scale2(ld_scale(src + kQ4OffScale + (lane & ~1)));
         if (lane < 8) rope = ld_row16(src + kQ4OffRope + 16 * lane);
         const uint32_t bias = q4_bias(s2);
         lo = q4_word(w.x, s2, bias);
