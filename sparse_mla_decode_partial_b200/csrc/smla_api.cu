@@ -1239,8 +1239,10 @@ smla_status smla_q4_append(const void *rows, int n_rows, const int32_t *cu_rows,
     p.pt_stride = pt_stride;
     p.num_pages = num_pages;
     p.cache = static_cast<uint8_t *>(cache_q4);
-    const int grid = (int)(((long long)n_rows + smla::kQ4Warps - 1) / smla::kQ4Warps);
-    const cudaError_t e = launch_dependent(smla::smla_q4_append_kernel, grid, 32 * smla::kQ4Warps, 0,
+    const bool many = smla::q4_many_rows(n_rows, current_device_sms());
+    const int per = smla::kQ4Warps * (many ? 4 : 1);
+    const int grid = (int)(((long long)n_rows + per - 1) / per);
+    const cudaError_t e = launch_dependent(many ? smla::smla_q4_append_kernel<4> : smla::smla_q4_append_kernel<1>, grid, 32 * smla::kQ4Warps, 0,
                                            static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
@@ -1253,7 +1255,9 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
     if (st != SMLA_OK) return st;
     if (!positions || !rows) return SMLA_ERR_INVALID_ARG;
     if (!aligned(positions, 4) || !aligned(rows, 16)) return SMLA_ERR_MISALIGNED;
-    const long long blocks = ((long long)B * K + smla::kQ4Warps - 1) / smla::kQ4Warps;
+    const bool many = smla::q4_many_rows((long long)B * K, current_device_sms());
+    const int per = smla::kQ4Warps * (many ? 4 : 1);
+    const long long blocks = ((long long)B * K + per - 1) / per;
     if (blocks > INT_MAX) return SMLA_ERR_INVALID_ARG;
     smla::Q4ReadParams p{};
     p.cache = static_cast<const uint8_t *>(cache_q4);
@@ -1264,7 +1268,7 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
     p.B = B;
     p.K = K;
     p.out = static_cast<__nv_bfloat16 *>(rows);
-    const cudaError_t e = launch_dependent(smla::smla_q4_read_kernel, (int)blocks, 32 * smla::kQ4Warps, 0,
+    const cudaError_t e = launch_dependent(many ? smla::smla_q4_read_kernel<4> : smla::smla_q4_read_kernel<1>, (int)blocks, 32 * smla::kQ4Warps, 0,
                                            static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }

@@ -78,11 +78,6 @@ __device__ __forceinline__ uint4 ld_row16(const uint8_t *p) {
                  : "l"(p));
     return v;
 }
-__device__ __forceinline__ uint2 ld_row8(const uint8_t *p) {
-    uint2 v;
-    asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 // A group's scale, as loaded; q4_scale2 makes it (scale, scale).  Kept apart: a
 // load meant to run ahead must not be followed by arithmetic on its result.
 __device__ __forceinline__ uint32_t ld_scale(const uint8_t *p) {
@@ -131,66 +126,108 @@ __device__ __forceinline__ float q4_scale_of(float a) {
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-constexpr int kQ4Warps = 8;  // rows per CTA, one warp each
+constexpr int kQ4Warps = 8;
 
-// One warp per row: lane l quantises latents 16 l .. 16 l + 15 (half a group),
-// lanes 0-7 also carry the rope values.  Bound by memory: 1152 bytes in, 416
-// out per row.
+// x / scale rounded to the nearest integer, ties to even, plus 8: a code, as the
+// low bits of kQ4CodeBits + code.  inv = 1 / scale correctly rounded, so x inv is
+// off by 2^-21 at most (|x / scale| <= 7).  x has eight significant bits and scale
+// four, so x / scale is either a half integer or at least 2^-10 away from one:
+// rounding to a multiple of 2^-11 first (the fma onto 1.5 * 2^12) gives half
+// integers exactly and moves nothing else across one.  The addition then rounds
+// to an integer, which stands in the low mantissa bits of 1.5 * 2^23 + code.
+// Two float operations where a true division takes about twenty instructions.
+constexpr uint32_t kQ4CodeBits = 0x4B400000u;  // 1.5 * 2^23
+__device__ __forceinline__ uint32_t q4_code(float x, float inv) {
+    return __float_as_uint(__fadd_rn(__fmaf_rn(x, inv, 6144.f), 12582912.f + 8.f - 6144.f));
+}
+
+// One warp per RPW rows, all their loads in flight at once: lane l quantises
+// words l and l + 32 of each (eight latents a word, four lanes a group), lanes
+// 0-7 also carry its rope values, and the warp finds where the rows go.
+// Every access covers whole 128-byte lines.  1152 bytes in, 416 out per row.
+template <int RPW>
 __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_append_kernel(const Q4AppendParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const long long i = (long long)blockIdx.x * kQ4Warps + (threadIdx.x >> 5);
-    if (i >= p.n_rows) return;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.rows + i * kD);
-    const uint4 a = ld_input(src + 2 * lane), b4 = ld_input(src + 2 * lane + 1);
-    uint4 rope = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < 8) rope = ld_input(src + kDc / 8 + lane);
-    if (i >= ld_input(p.cu_rows + p.B)) return;  // rows behind the last sequence
-    int lo = 0, hi = p.B - 1;                    // the last sequence with cu_rows[b] <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (ld_input(p.cu_rows + mid) <= i) lo = mid; else hi = mid - 1;
-    }
-    const int first = ld_input(p.cu_rows + lo);
-    long long row = -1;
-    if (first >= 0 && first <= i && i < ld_input(p.cu_rows + lo + 1))
-        row = paged_row(p.page_table + (size_t)lo * p.pt_stride, p.pt_stride, p.num_pages,
-                        (long long)ld_input(p.start + lo) + (i - first));
-    if (row < 0) {
-        if (lane == 0) count_bad_index();
-        return;
-    }
-    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b4.x, b4.y, b4.z, b4.w};
-    // largest magnitude of the group (bit patterns of magnitudes order as
-    // integers, infinities and NaN above every finite value)
-    uint32_t top = 0;
+    const long long i0 = ((long long)blockIdx.x * kQ4Warps + (threadIdx.x >> 5)) * RPW;
+    if (i0 >= p.n_rows) return;
+    const int rows = (int)min((long long)RPW, p.n_rows - i0);
+    uint4 in[RPW][2], rope[RPW];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float most = __uint_as_float(top << 16);
-    const bool bad = !(most < 0x1p120f);
-    const bool live = !bad && most >= 0x1p-118f;
-    const float scale = live ? q4_scale_of(most) : 0.f;
-    uint32_t w[2] = {0x88888888u, 0x88888888u};
-    if (live) {
+    for (int k = 0; k < RPW; ++k) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.rows + (i0 + (k < rows ? k : 0)) * kD);
+        in[k][0] = ld_input(src + lane);
+        in[k][1] = ld_input(src + 32 + lane);
+        rope[k] = ld_input(src + kDc / 8 + (lane & 7));
+    }
+    // The sequence of row i0, the last one with cu_rows[b] <= i0: the warp tries
+    // 32 boundaries at a time, so that up to 32 sequences cost one round trip.
+    const int end = ld_input(p.cu_rows + p.B);
+    int lo = 0;
+    for (int n = p.B; n > 1;) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool before = lane * step < n && ld_input(p.cu_rows + at) <= i0;
+        const uint32_t v = __ballot_sync(0xffffffffu, before);
+        const int k = v ? 31 - __clz(v) : 0;
+        n = min(n - k * step, step);
+        lo += k * step;
+    }
+    long long where = -1;  // lane k: row of the pool that row i0 + k goes to
+    if (lane < rows && i0 + lane < end) {  // rows behind the last sequence go nowhere
+        const long long i = i0 + lane;
+        int first = ld_input(p.cu_rows + lo), next = ld_input(p.cu_rows + lo + 1);
+        while (i >= next && lo + 1 < p.B) {  // the next sequences may be empty
+            ++lo;
+            first = next;
+            next = ld_input(p.cu_rows + lo + 1);
+        }
+        if (first >= 0 && first <= i && i < next)
+            where = paged_row(p.page_table + (size_t)lo * p.pt_stride, p.pt_stride, p.num_pages,
+                              (long long)ld_input(p.start + lo) + (i - first));
+        if (where < 0) count_bad_index();
+    }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            w[k] = 0;
+    for (int k = 0; k < RPW; ++k) {
+        const long long row = __shfl_sync(0xffffffffu, where, k);
+        if (row < 0) continue;
+        uint8_t *dst = p.cache + row * kQ4RowBytes;
+        bool bad = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t v[4] = {in[k][h].x, in[k][h].y, in[k][h].z, in[k][h].w};
+            // largest magnitude of the group (bit patterns of magnitudes order
+            // as integers, infinities and NaN above every finite value)
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = __vmaxu2(top, v[j] & 0x7FFF7FFFu);
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float most = __uint_as_float(top << 16);
+            const bool finite = most < 0x1p120f;
+            const bool live = finite && most >= 0x1p-118f;
+            bad = bad || !finite;
+            const float scale = live ? q4_scale_of(most) : 0.f;
+            const float inv = live ? __frcp_rn(scale) : 0.f;
+            // kQ4CodeBits shifted to every nibble and added up, taken off beforehand
+            uint32_t w = 0u - kQ4CodeBits * 0x11111111u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int c0 = (int)rintf(__fdiv_rn(bf16_lo(v[4 * k + j]), scale)) + 8;
-                const int c1 = (int)rintf(__fdiv_rn(bf16_hi(v[4 * k + j]), scale)) + 8;
-                w[k] |= (uint32_t)c0 << (4 * j) | (uint32_t)c1 << (4 * j + 16);
+                const uint32_t x = finite ? v[j] : 0u;  // (inf * 0 would be no code)
+                w += q4_code(bf16_lo(x), inv) << (4 * j);
+                w += q4_code(bf16_hi(x), inv) << (4 * j + 16);
             }
+            *reinterpret_cast<uint32_t *>(dst + 128 * h + 4 * lane) = w;
+            if ((lane & 3) == 0)
+                *reinterpret_cast<uint16_t *>(dst + kQ4OffScale + 16 * h + (lane >> 1)) =
+                    (uint16_t)(__float_as_uint(scale) >> 16);
         }
+        const bool poison = __any_sync(0xffffffffu, bad);
+        if (lane < 8)
+            *reinterpret_cast<uint4 *>(dst + kQ4OffRope + 16 * lane) =
+                poison ? make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu) : rope[k];
     }
-    uint8_t *dst = p.cache + row * kQ4RowBytes;
-    *reinterpret_cast<uint2 *>(dst + 8 * lane) = make_uint2(w[0], w[1]);
-    if ((lane & 1) == 0)
-        *reinterpret_cast<uint16_t *>(dst + kQ4OffScale + lane) = (uint16_t)(__float_as_uint(scale) >> 16);
-    if (__any_sync(0xffffffffu, bad)) rope = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-    if (lane < 8) *reinterpret_cast<uint4 *>(dst + kQ4OffRope + 16 * lane) = rope;
 }
 
 // ---------------------------------------------------------------- read back
@@ -204,34 +241,59 @@ struct Q4ReadParams {
     __nv_bfloat16 *out;     // [B, K, 576]
 };
 
-// One warp per listed position: lane l decodes latents 16 l .. 16 l + 15,
-// lanes 0-7 copy the rope values.  Bound by memory: 416 bytes in, 1152 out.
+// One warp per RPW listed positions, all their loads in flight at once: lane l
+// decodes words l and l + 32 of each, lanes 0-7 copy the rope values.  416 bytes
+// in, 1152 out per row.
+template <int RPW>
 __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_read_kernel(const Q4ReadParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const long long i = (long long)blockIdx.x * kQ4Warps + (threadIdx.x >> 5);
-    if (i >= (long long)p.B * p.K) return;
-    const int pos = ld_input(p.positions + i);
-    long long row = -1;
-    if (pos != -1) {
-        row = paged_row(p.page_table + (size_t)(i / p.K) * p.pt_stride, p.pt_stride, p.num_pages, pos);
-        if (row < 0 && lane == 0) count_bad_index();
+    const long long n = (long long)p.B * p.K;
+    const long long i0 = ((long long)blockIdx.x * kQ4Warps + (threadIdx.x >> 5)) * RPW;
+    if (i0 >= n) return;
+    long long where = -1;
+    if (lane < RPW && i0 + lane < n) {
+        const long long i = i0 + lane;
+        const int pos = ld_input(p.positions + i);
+        if (pos != -1) {
+            where = paged_row(p.page_table + (size_t)(i / p.K) * p.pt_stride, p.pt_stride, p.num_pages, pos);
+            if (where < 0) count_bad_index();
+        }
     }
-    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo, rope = lo;
-    if (row >= 0) {
-        const uint8_t *src = p.cache + row * kQ4RowBytes;
-        const uint2 w = ld_row8(src + 8 * lane);
-        const uint32_t s2 = q4_scale2(ld_scale(src + kQ4OffScale + (lane & ~1)));
-        if (lane < 8) rope = ld_row16(src + kQ4OffRope + 16 * lane);
-        const uint32_t bias = q4_bias(s2);
-        lo = q4_word(w.x, s2, bias);
-        hi = q4_word(w.y, s2, bias);
+    uint32_t w[RPW][2], scale[RPW][2];
+    uint4 rope[RPW];
+#pragma unroll
+    for (int k = 0; k < RPW; ++k) {
+        const long long row = __shfl_sync(0xffffffffu, where, k);
+        rope[k] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[k][h] = scale[k][h] = 0u;  // no row: zeros
+            if (row >= 0) {
+                const uint8_t *src = p.cache + row * kQ4RowBytes;
+                asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(w[k][h]) : "l"(src + 128 * h + 4 * lane));
+                scale[k][h] = ld_scale(src + kQ4OffScale + 16 * h + 2 * (lane >> 2));
+            }
+        }
+        if (row >= 0) rope[k] = ld_row16(p.cache + row * kQ4RowBytes + kQ4OffRope + 16 * (lane & 7));
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(p.out + i * kD);
-    dst[2 * lane] = lo;
-    dst[2 * lane + 1] = hi;
-    if (lane < 8) dst[kDc / 8 + lane] = rope;
+#pragma unroll
+    for (int k = 0; k < RPW; ++k) {
+        if (i0 + k >= n) break;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (i0 + k) * kD);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t s2 = q4_scale2(scale[k][h]);
+            dst[32 * h + lane] = q4_word(w[k][h], s2, q4_bias(s2));
+        }
+        if (lane < 8) dst[kDc / 8 + lane] = rope[k];
+    }
 }
+
+// Rows per warp: four keep more loads in flight, once there are rows enough
+// for every SM to hold several such warps; below that, one row per warp has the
+// shorter chain.
+__host__ inline bool q4_many_rows(long long rows, int sms) { return rows >= (long long)sms * kQ4Warps * 4 * 4; }
 
 }  // namespace smla

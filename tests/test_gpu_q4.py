@@ -90,6 +90,35 @@ def test_append_error_is_at_most_half_a_step():
     assert (x[:, 512:] == v[:, 512:]).all()
 
 
+def test_append_and_read_many_rows():
+    """Enough rows for four per warp, ragged, with rows behind the last sequence."""
+    new, start = [9001, 0, 13003, 1], [7, 0, 60, 63]
+    paged = cu.Paged([a + n for a, n in zip(start, new)], seed=1)
+    n = sum(new)
+    rows = cu.latents(n + 3, 12)
+    cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+    offs = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+    binding.q4_append(rows.cuda(), cache, paged.cuda, offs, torch.tensor(start, dtype=torch.int32).cuda())
+    lists = torch.full((4, max(new) + 1), -1, dtype=torch.int32)
+    for b in range(4):
+        lists[b, :new[b]] = torch.arange(start[b], start[b] + new[b]).flip(0).int()
+    out = cu.f64(binding.q4_read(cache, paged.cuda, lists.cuda()))
+    raw = cache.cpu().numpy().reshape(-1, cu.ROW)
+    at = 0
+    assert not out[1].any()
+    for b in (0, 2, 3):
+        mine = raw[paged.rows(b, range(start[b], start[b] + new[b]))]
+        some = np.unique(np.linspace(0, new[b] - 1, 97).astype(int))
+        np.testing.assert_array_equal(mine[some], cu.quantise(rows[at + torch.from_numpy(some)]))
+        np.testing.assert_array_equal(out[b, :new[b]], cu.values(mine)[::-1])
+        assert not out[b, new[b]:].any()
+        at += new[b]
+    used = np.concatenate([paged.rows(b, range(start[b], start[b] + new[b])) for b in range(4)])
+    left = np.ones(len(raw), bool)
+    left[used] = False
+    assert not raw[left].any()
+
+
 def test_append_counts_rows_it_cannot_place():
     paged = cu.Paged([64, 64, 64])
     paged.table[1, 0] = -1
