@@ -114,12 +114,13 @@ struct Q4AppendParams {
     uint8_t *cache;             // [num_pages * 64, 416]
 };
 
-// Smallest number of four significant bits >= a / 7 (a in [2^-118, 2^120)).
-// a and 7 s are multiples of a common step that is at least 2^-12 of them, so
-// the correctly rounded quotient is above, at or below a candidate exactly
-// when the real one is.
+// Smallest number of four significant bits >= a / 7 (a in [2^-118, 2^120), eight
+// significant bits).  a / 7 either is such a number or differs from every one of
+// them by 2^-12 of itself at least, so a / 7 less 2^-20 of itself (one product,
+// its rounding included) lies above exactly the candidates below a / 7; rounding
+// its mantissa up to three bits then gives the answer.
 __device__ __forceinline__ float q4_scale_of(float a) {
-    const uint32_t u = __float_as_uint(__fdiv_rn(a, 7.f));
+    const uint32_t u = __float_as_uint(__fmul_rn(a, (float)((1.0 - 0x1p-20) / 7.0)));
     return __uint_as_float((u + 0x000FFFFFu) & 0xFFF00000u);
 }
 
@@ -129,13 +130,18 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 constexpr int kQ4Warps = 8;
 
 // x / scale rounded to the nearest integer, ties to even, plus 8: a code, as the
-// low bits of kQ4CodeBits + code.  inv = 1 / scale correctly rounded, so x inv is
-// off by 2^-21 at most (|x / scale| <= 7).  x has eight significant bits and scale
+// low bits of kQ4CodeBits + code.  inv is 1 / scale to within 2^-22 of itself, so
+// x inv is off by 2^-18 at most (|x / scale| <= 7).  x has eight significant bits and scale
 // four, so x / scale is either a half integer or at least 2^-10 away from one:
 // rounding to a multiple of 2^-11 first (the fma onto 1.5 * 2^12) gives half
 // integers exactly and moves nothing else across one.  The addition then rounds
 // to an integer, which stands in the low mantissa bits of 1.5 * 2^23 + code.
 // Two float operations where a true division takes about twenty instructions.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 constexpr uint32_t kQ4CodeBits = 0x4B400000u;  // 1.5 * 2^23
 __device__ __forceinline__ uint32_t q4_code(float x, float inv) {
     return __float_as_uint(__fadd_rn(__fmaf_rn(x, inv, 6144.f), 12582912.f + 8.f - 6144.f));
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_append_kernel(const Q4A
             const bool live = finite && most >= 0x1p-118f;
             bad = bad || !finite;
             const float scale = live ? q4_scale_of(most) : 0.f;
-            const float inv = live ? __frcp_rn(scale) : 0.f;
+            const float inv = live ? fast_rcp(scale) : 0.f;
             // kQ4CodeBits shifted to every nibble and added up, taken off beforehand
             uint32_t w = 0u - kQ4CodeBits * 0x11111111u;
 #pragma unroll
