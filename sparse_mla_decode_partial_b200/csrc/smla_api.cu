@@ -29,6 +29,7 @@
 #include "smla_indexer.cuh"
 #include "smla_evict.cuh"
 #include "smla_partial_q4.cuh"
+#include "smla_weigh.cuh"
 
 namespace {
 
@@ -1403,14 +1404,25 @@ static_assert(smla::kEvictBuffers == SMLA_EVICT_MAX_CACHES, "caches per apply ca
 
 namespace {
 
-template <bool Q4, int HG>
-cudaError_t launch_weigh_rows(const smla::WeighParams &p, int grid, cudaStream_t st) {
+template <int HG>
+cudaError_t launch_weigh_rows(const smla::WeighOld &p, int grid, cudaStream_t st) {
     using C = smla::WeighCfg<HG>;
     const cudaError_t e = ensure_smem_attr(
-        reinterpret_cast<const void *>(&smla::smla_evict_weigh_kernel<Q4, HG>), C::kSmemBytes);
+        reinterpret_cast<const void *>(&smla::smla_evict_weigh_kernel<HG>), C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_dependent(smla::smla_evict_weigh_kernel<Q4, HG>, grid, 32 * smla::kWeighWarps,
+    return launch_dependent(smla::smla_evict_weigh_kernel<HG>, grid, 32 * smla::kWeighWarps,
                             C::kSmemBytes, st, p);
+}
+
+template <int G>
+cudaError_t launch_weigh_q4(smla::WeighParams &a, cudaStream_t st) {
+    using C = smla::WeighQ4Cfg<G>;
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_weigh_q4_kernel<G>), C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const long long tiles = a.p.B * (((long long)a.p.K + C::kTile - 1) / C::kTile);
+    a.grid = (int)std::min<long long>(tiles, (long long)C::kMinBlocks * current_device_sms());
+    a.min_tiles = 2;
+    return launch_dependent(smla::smla_weigh_q4_kernel<G>, a.grid, C::kThreads, C::kSmemBytes, st, a);
 }
 
 template <bool Q4>
@@ -1426,7 +1438,22 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
     if (!q || !seq_lens || !lse || !acc) return SMLA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(acc, 4))
         return SMLA_ERR_MISALIGNED;
-    smla::WeighParams p{};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long rows = (long long)T * H;
+    cudaError_t e;
+    if (Q4) {
+        smla::WeighParams a{};
+        a.p = make_params(q, cache, num_pages, page_table, pt_stride, nullptr, B, 1, (int)rows, max_n, scale, 1);
+        a.p.seq_lens = seq_lens;
+        a.p.pack = a.p.dense_t = T;
+        a.p.dense_h = H;
+        a.lse = lse;
+        a.acc = acc;
+        if (B * ((max_n + 63ll) / 64) > INT_MAX) return SMLA_ERR_INVALID_ARG;
+        e = rows <= 16 ? launch_weigh_q4<1>(a, st) : rows <= 32 ? launch_weigh_q4<2>(a, st) : launch_weigh_q4<4>(a, st);
+        return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+    }
+    smla::WeighOld p{};
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.cache = static_cast<const uint8_t *>(cache);
     p.num_pages = num_pages;
@@ -1445,11 +1472,9 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
     p.nchunk = (int)std::max<long long>(1, std::min<long long>(most, (2ll * current_device_sms() + B - 1) / B));
     if ((long long)B * p.nchunk > INT_MAX) return SMLA_ERR_INVALID_ARG;
     const int grid = B * p.nchunk;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long rows = (long long)T * H;
-    const cudaError_t e = rows <= 16   ? launch_weigh_rows<Q4, 1>(p, grid, st)
-                          : rows <= 32 ? launch_weigh_rows<Q4, 2>(p, grid, st)
-                                       : launch_weigh_rows<Q4, 4>(p, grid, st);
+    e = rows <= 16   ? launch_weigh_rows<1>(p, grid, st)
+        : rows <= 32 ? launch_weigh_rows<2>(p, grid, st)
+                     : launch_weigh_rows<4>(p, grid, st);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 

@@ -1,7 +1,6 @@
 // smla_evict.cuh -- eviction from the paged cache by accumulated attention
-// weight: the weight every cached position has received is accumulated from a
-// decode's queries and lse, the positions that received least are chosen, and
-// the rows that stay fill the holes they leave.
+// weight: the positions that received least are chosen, and the rows that stay
+// fill the holes they leave.  (smla_weigh.cuh accumulates the weights.)
 #pragma once
 
 #include <cstdint>
@@ -11,219 +10,6 @@
 #include "smla_q4.cuh"
 
 namespace smla {
-
-// ---------------------------------------------------------------- accumulate
-// acc[b, i] += sum over the query rows (t, h) of sequence b with i visible of
-//   exp(scale q[b,t,h] . row_i - lse[b,t,h]).
-struct WeighParams {
-    const __nv_bfloat16 *q;   // [B, T, H, 576]
-    const uint8_t *cache;     // bf16 rows of 1152 bytes or 4-bit rows of 416
-    long long num_pages;
-    const int *page_table;    // [B, pt_stride]
-    int pt_stride;
-    const int *seq_lens;      // [B, T]
-    const float *lse;         // [B, T, H]
-    int B, T, H;
-    float scale_log2;
-    float *acc;               // [B, max_n]
-    int max_n;
-    int nchunk;               // CTAs per sequence
-};
-
-constexpr int kWeighWarps = 8;
-constexpr int kWeighTile = 32;  // cache rows per warp and step
-
-template <int HG>
-struct WeighCfg {
-    static constexpr int kRows = 16 * HG;  // query rows per pass
-    static constexpr int kOffFrag = 0;     // uint4 [36][HG][32]: A fragments in lane order
-    static constexpr int kOffLse = 36 * HG * 512;       // float2 [kRows]: lse in log2 units, high and low part
-    static constexpr int kOffLim = kOffLse + kRows * 8;  // int [kRows]: visible positions
-    static constexpr int kSmemBytes = kOffLim + kRows * 4;
-};
-
-// First of the four dims that lane column c feeds to k16 step s (dims +0, +1
-// go to k = 2 c, 2 c + 1 and dims +2, +3 to k = 2 c + 8, 2 c + 9).  The sum
-// over k does not care for the order of the dims, so each lane takes dims it
-// can load as 16 consecutive bytes: 8 bf16 values (two steps) or one whole
-// group of 32 codes (eight steps, one scale).
-template <bool Q4>
-__device__ __forceinline__ int weigh_dim(int s, int c) {
-    if (Q4 && s < 32) return 32 * (4 * (s >> 3) + c) + 8 * ((s & 7) >> 1) + 4 * (s & 1);
-    return 32 * (s >> 1) + 8 * c + 4 * (s & 1);
-}
-
-// One warp: the scores of 32 cache rows (half a page, consecutive rows)
-// against 16 HG query rows by mma.sync, the cache rows (N) straight from
-// global memory into B fragments, the query rows (M) from shared memory.
-template <bool Q4, int HG>
-__device__ __forceinline__ void weigh_scores(const uint8_t *row0, const uint4 *frag, int lane,
-                                             float (&s)[HG][4][4]) {
-    const int c = lane & 3;
-    constexpr int kRow = Q4 ? kQ4RowBytes : kRowBytes;
-    const uint8_t *mine = row0 + (lane >> 2) * kRow;
-#pragma unroll
-    for (int g = 0; g < HG; ++g)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) s[g][n][0] = s[g][n][1] = s[g][n][2] = s[g][n][3] = 0.f;
-    auto step = [&](int st, const uint32_t (&b0)[4], const uint32_t (&b1)[4]) {
-#pragma unroll
-        for (int g = 0; g < HG; ++g) {
-            const uint4 a = frag[(st * HG + g) * 32 + lane];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mma_bf16_16816(s[g][n], a.x, a.y, a.z, a.w, b0[n], b1[n]);
-        }
-    };
-    auto chunk = [&](int st, const uint4 (&v)[4]) {  // 8 bf16 values per lane: two k16 steps
-        const uint32_t x[4] = {v[0].x, v[1].x, v[2].x, v[3].x}, y[4] = {v[0].y, v[1].y, v[2].y, v[3].y};
-        const uint32_t z[4] = {v[0].z, v[1].z, v[2].z, v[3].z}, w[4] = {v[0].w, v[1].w, v[2].w, v[3].w};
-        step(st, x, y);
-        step(st + 1, z, w);
-    };
-    if constexpr (Q4) {
-        uint4 code[4], next[4];
-        uint32_t sc[4], next_sc[4];
-        auto load = [&](int j, uint4 (&d)[4], uint32_t (&s2)[4]) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                d[n] = ld_row16(mine + n * 8 * kRow + 16 * (4 * j + c));
-                s2[n] = ld_scale(mine + n * 8 * kRow + kQ4OffScale + 2 * (4 * j + c));
-            }
-        };
-        load(0, code, sc);
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            if (j < 3) {
-                load(j + 1, next, next_sc);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) next[n] = ld_row16(mine + n * 8 * kRow + kQ4OffRope + 16 * c);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint4 v[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const uint32_t word = w == 0 ? code[n].x : w == 1 ? code[n].y : w == 2 ? code[n].z : code[n].w;
-                    const uint32_t s2 = q4_scale2(sc[n]);
-                    v[n] = q4_word(word, s2, q4_bias(s2));
-                }
-                chunk(8 * j + 2 * w, v);
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                code[n] = next[n];
-                sc[n] = next_sc[n];
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) next[n] = ld_row16(mine + n * 8 * kRow + kQ4OffRope + 64 + 16 * c);
-        chunk(32, code);
-        chunk(34, next);
-    } else {
-#pragma unroll 1
-        for (int j = 0; j < 18; j += 3) {
-            uint4 v[3][4];
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) v[k][n] = ld_row16(mine + n * 8 * kRow + 64 * (j + k) + 16 * c);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) chunk(2 * (j + k), v[k]);
-        }
-    }
-}
-
-template <bool Q4, int HG>
-__global__ void __launch_bounds__(32 * kWeighWarps) smla_evict_weigh_kernel(const WeighParams p) {
-    using C = WeighCfg<HG>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint4 *frag = reinterpret_cast<uint4 *>(smem + C::kOffFrag);
-    float2 *lse_s = reinterpret_cast<float2 *>(smem + C::kOffLse);
-    int *lim_s = reinterpret_cast<int *>(smem + C::kOffLim);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
-    const int b = blockIdx.x / p.nchunk, part = blockIdx.x % p.nchunk;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    int len = 0;  // longest visible length of the sequence's query tokens
-    for (int t = 0; t < p.T; ++t) {
-        const int raw = ld_input(p.seq_lens + (size_t)b * p.T + t);
-        len = max(len, min(max(raw, 0), p.max_n));
-        if (part == 0 && threadIdx.x == t % blockDim.x && (raw < 0 || raw > p.max_n)) count_bad_index();
-    }
-    const int tiles = (len + kWeighTile - 1) / kWeighTile;
-    const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
-    const int rows = p.T * p.H;
-    constexpr int kRow = Q4 ? kQ4RowBytes : kRowBytes;
-
-    for (int g0 = 0; g0 < rows; g0 += C::kRows) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 36 * HG * 32; i += blockDim.x) {
-            const int l = i & 31, g = (i >> 5) % HG, st = i / (32 * HG);
-            const int r = g0 + 16 * g + (l >> 2), d = weigh_dim<Q4>(st, l & 3);
-            const __nv_bfloat16 *q = p.q + ((size_t)b * rows + r) * kD + d;
-            uint2 lo = make_uint2(0u, 0u), hi = lo;
-            if (r < rows) lo = *reinterpret_cast<const uint2 *>(q);
-            if (r + 8 < rows) hi = *reinterpret_cast<const uint2 *>(q + 8 * kD);
-            frag[i] = make_uint4(lo.x, hi.x, lo.y, hi.y);
-        }
-        for (int i = threadIdx.x; i < C::kRows; i += blockDim.x) {
-            const int r = g0 + i;
-            float2 l2 = make_float2(0.f, 0.f);
-            int lim = 0;
-            if (r < rows) {
-                const float l = p.lse[(size_t)b * rows + r];
-                // lse in log2 units as a sum of two floats: its rounding would
-                // otherwise scale every weight of the row
-                const double x = (double)l * 1.4426950408889634074;
-                l2.x = (float)x;
-                l2.y = isfinite(l2.x) ? (float)(x - (double)l2.x) : 0.f;
-                // a row that attended to nothing (lse = -inf) gives no weight
-                lim = l == -INFINITY ? 0 : min(max(ld_input(p.seq_lens + (size_t)b * p.T + r / p.H), 0), p.max_n);
-            }
-            lse_s[i] = l2;
-            lim_s[i] = lim;
-        }
-        __syncthreads();
-        for (int tile = part * kWeighWarps + warp; tile < tiles; tile += p.nchunk * kWeighWarps) {
-            const int pos0 = tile * kWeighTile;
-            const long long row = paged_row(pt_b, p.pt_stride, p.num_pages, pos0);
-            if (row < 0) {
-                if (g0 == 0 && lane < min(kWeighTile, len - pos0)) count_bad_index();
-                continue;
-            }
-            float s[HG][4][4];
-            weigh_scores<Q4, HG>(p.cache + row * kRow, frag, lane, s);
-            float w[8];  // column 8 n + 2 c + e at [2 n + e]
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = 0.f;
-#pragma unroll
-            for (int g = 0; g < HG; ++g) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = 16 * g + 8 * h + (lane >> 2);
-                    const float2 l2 = lse_s[r];
-                    const int lim = lim_s[r] - pos0 - 2 * c;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float x = fmaf(s[g][k >> 1][2 * h + (k & 1)], p.scale_log2, -l2.x) - l2.y;
-                        w[k] += 8 * (k >> 1) + (k & 1) < lim ? fast_exp2(x) : 0.f;
-                    }
-                }
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] += __shfl_xor_sync(0xffffffffu, w[k], o);
-            float v = w[0];
-#pragma unroll
-            for (int k = 1; k < 8; ++k) v = (lane >> 2) == k ? w[k] : v;
-            const int pos = pos0 + 8 * (lane >> 3) + 2 * c + ((lane >> 2) & 1);
-            if (pos < len) p.acc[(size_t)b * p.max_n + pos] += v;
-        }
-    }
-}
 
 // ---------------------------------------------------------------- plan
 // Per sequence of n slots: the min(n, K) slots that stay, and for each slot

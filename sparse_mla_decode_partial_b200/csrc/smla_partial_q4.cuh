@@ -125,6 +125,60 @@ __device__ __forceinline__ uint32_t bf16x2_pow2(float d) {
     return (uint32_t)(e << 7) * 0x00010001u;
 }
 
+// Raw scores of 16 cache rows (those at `rows`, 416 bytes apart) against 16 G
+// query rows, whose A fragments are uint4 [36][G][32] at q.  s[g][i]: query rows
+// 16 g + r, + 8 against columns 2 c, 2 c + 1 of the i-th n8 tile.  Each fragment
+// of the cache is decoded once for all G.
+template <int G>
+__device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, float (&s)[G][2][4]) {
+    const int c = lane & 3;
+    const uint32_t row = rows + q4_row_of(lane >> 2) * kQ4RowBytes;
+    q += 16 * lane;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s[g][i][0] = s[g][i][1] = s[g][i][2] = s[g][i][3] = 0.f;
+    auto steps = [&](int st, const uint4 (&v)[2]) {  // k16 steps st, st + 1
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint4 a0 = lds_16(q + (st * G + g) * 512), a1 = lds_16(q + ((st + 1) * G + g) * 512);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mma_bf16_16816(s[g][i], a0.x, a0.y, a0.z, a0.w, v[i].x, v[i].y);
+                mma_bf16_16816(s[g][i], a1.x, a1.y, a1.z, a1.w, v[i].z, v[i].w);
+            }
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t s2[2], bias[2];
+        uint4 code[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            code[i] = lds_16(row + i * 8 * kQ4RowBytes + 16 * (4 * j + c));
+            s2[i] = lds_u16x2(row + i * 8 * kQ4RowBytes + kQ4OffScale + 2 * (4 * j + c));
+            bias[i] = q4_bias(s2[i]);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint4 v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t word = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
+                v[i] = q4_word(word, s2[i], bias[i]);
+            }
+            steps(8 * j + 2 * w, v);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint4 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = lds_16(row + i * 8 * kQ4RowBytes + kQ4OffRope + 64 * j + 16 * c);
+        steps(32 + 2 * j, v);
+    }
+}
+
 // One warp's share of a CTA: scores of 16 rows, 128 output columns.
 struct Q4Consumer {
     int warp, lane, r, c;
@@ -145,47 +199,6 @@ struct Q4Consumer {
         l0 = l1 = 0.f;
 #pragma unroll
         for (int n = 0; n < 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
-    }
-
-    // Raw scores of this warp's 16 rows against 16 query rows.
-    __device__ __forceinline__ void scores(uint32_t q_addr, uint32_t tile, float (&s)[2][4]) {
-        const uint32_t row = tile + (16 * warp + q4_row_of(r)) * kQ4RowBytes;
-        const uint32_t q = q_addr + 16 * lane;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t s2[2], bias[2];
-            uint4 code[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                code[i] = lds_16(row + i * 8 * kQ4RowBytes + 16 * (4 * j + c));
-                s2[i] = lds_u16x2(row + i * 8 * kQ4RowBytes + kQ4OffScale + 2 * (4 * j + c));
-                bias[i] = q4_bias(s2[i]);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint4 a0 = lds_16(q + (8 * j + 2 * w) * 512);
-                const uint4 a1 = lds_16(q + (8 * j + 2 * w + 1) * 512);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t word = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
-                    const uint4 v = q4_word(word, s2[i], bias[i]);
-                    mma_bf16_16816(s[i], a0.x, a0.y, a0.z, a0.w, v.x, v.y);
-                    mma_bf16_16816(s[i], a1.x, a1.y, a1.z, a1.w, v.z, v.w);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint4 a0 = lds_16(q + (32 + 2 * j) * 512), a1 = lds_16(q + (33 + 2 * j) * 512);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 v = lds_16(row + i * 8 * kQ4RowBytes + kQ4OffRope + 64 * j + 16 * c);
-                mma_bf16_16816(s[i], a0.x, a0.y, a0.z, a0.w, v.x, v.y);
-                mma_bf16_16816(s[i], a1.x, a1.y, a1.z, a1.w, v.z, v.w);
-            }
-        }
     }
 
     // Masked scores (log2 units, -inf where masked) -> P in this warp's rows'
@@ -303,13 +316,14 @@ struct Q4Consumer {
     }
 };
 
-// Stage 16 query rows (row0 .. row0 + nrows - 1 of q; the rest zero) as A
-// fragments in lane order.
+// Stage 16 G query rows (row0 .. row0 + nrows - 1 of q; the rest zero) as A
+// fragments in lane order, by NT threads.
+template <int G, int NT>
 __device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q, long long row0, int nrows) {
     uint4 *frag = reinterpret_cast<uint4 *>(dst);
 #pragma unroll
-    for (int k = 0; k < 9; ++k) {
-        const int i = threadIdx.x + 128 * k, l = i & 31, st = i >> 5, r = l >> 2;
+    for (int k = 0; k < 36 * G * 32 / NT; ++k) {
+        const int i = threadIdx.x + NT * k, l = i & 31, g = (i >> 5) % G, st = i / (32 * G), r = 16 * g + (l >> 2);
         const __nv_bfloat16 *src = q + (row0 + r) * kD + q4_dim_of(st, l & 3);
         uint2 lo = make_uint2(0u, 0u), hi = lo;
         if (r < nrows)
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
         const int tiles = (n + C::kTile - 1) / C::kTile;
         issue(it, 0, n);
         if (!staged) {
-            q4_stage_q(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
+            q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
             staged = true;
             __syncthreads();
         }
@@ -381,8 +395,9 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
             const uint32_t tile = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
             if (t + 1 < tiles && t == 0) issue(it + 1, 1, n);
             mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
-            float sc[2][4];
-            w.scores(sbase + C::kOffQ, tile, sc);
+            float sg[1][2][4];
+            q4_scores<1>(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sg);
+            float (&sc)[2][4] = sg[0];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -465,6 +480,69 @@ __host__ __device__ __forceinline__ int q4_sharers(int grid, int min_tiles, long
     return (int)(most < 1 ? 1 : most < grid ? most : grid);
 }
 
+// A CTA's run [begin, end) of the flattened tiles of TILE positions: total
+// first, then the unit and the tile it starts in.  Every thread calls it;
+// scratch holds 48 ints of shared memory.  count: report bad lengths (one CTA).
+struct Q4Run {
+    long long total, begin, end;
+    int unit, tile;
+};
+template <int TILE>
+__device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int n_units, int grid, int min_tiles,
+                                             int *prefix, int *scratch) {
+    const bool first_cta = blockIdx.x == 0;
+    Q4Run r{};
+    for (int u0 = 0; u0 < n_units; u0 += blockDim.x) {
+        const int u = u0 + threadIdx.x;
+        const int tiles = u < n_units ? (q4_unit_len(p, u, first_cta) + TILE - 1) / TILE : 0;
+        int sum;
+        const int incl = ix_block_scan(tiles, scratch, &sum);
+        if (prefix != nullptr && first_cta && u < n_units) prefix[u] = (int)r.total + incl - tiles;
+        r.total += sum;
+    }
+    if (prefix != nullptr && first_cta && threadIdx.x == 0) prefix[n_units] = (int)r.total;
+    const int sharers = q4_sharers(grid, min_tiles, r.total);
+    if ((int)blockIdx.x >= sharers || r.total == 0) return r;
+    r.begin = r.total * blockIdx.x / sharers;
+    r.end = r.total * (blockIdx.x + 1) / sharers;
+    long long before = 0;
+    for (int u0 = 0; u0 < n_units && before <= r.begin; u0 += blockDim.x) {
+        const int u = u0 + threadIdx.x;
+        const int tiles = u < n_units ? (q4_unit_len(p, u, false) + TILE - 1) / TILE : 0;
+        int sum;
+        const int incl = ix_block_scan(tiles, scratch, &sum);
+        const long long first = before + incl - tiles;
+        if (first <= r.begin && r.begin < first + tiles) {
+            scratch[40] = u;
+            scratch[41] = (int)(r.begin - first);
+        }
+        before += sum;
+    }
+    __syncthreads();
+    r.unit = scratch[40];
+    r.tile = scratch[41];
+    return r;
+}
+
+// Page of tile t of the sequence whose page-table row is pt_b; -1 where none is mapped.
+__device__ __forceinline__ int q4_page(const int *pt_b, int pt_stride, long long num_pages, int t) {
+    if (t >= pt_stride) return -1;
+    const int pg = ld_input(pt_b + t);
+    return (pg >= 0 && (long long)pg < num_pages) ? pg : -1;
+}
+
+// Thread 0: copy a page of 4-bit rows to shared memory at dst, or (no page)
+// complete its barrier at once.
+__device__ __forceinline__ void q4_copy_page(const PartialParams &p, int pg, uint8_t *dst, uint64_t *bar) {
+    if (pg < 0) {
+        mbar_arrive(bar);
+        return;
+    }
+    mbar_arrive_expect_tx(bar, (uint32_t)Q4Cfg::kStageBytes);
+    bulk_g2s(dst, reinterpret_cast<const uint8_t *>(p.cache) + (size_t)pg * Q4Cfg::kStageBytes,
+             (uint32_t)Q4Cfg::kStageBytes, bar);
+}
+
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_dense_kernel(const Q4Params a) {
     using C = Q4Cfg;
     const PartialParams &p = a.p;
@@ -481,66 +559,23 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this CTA's run of tiles: total first, then the unit it starts in
-    long long total = 0;
-    for (int u0 = 0; u0 < a.n_units; u0 += C::kThreads) {
-        const int u = u0 + tid;
-        const int tiles = u < a.n_units ? (q4_unit_len(p, u, blockIdx.x == 0) + C::kTile - 1) / C::kTile : 0;
-        int sum;
-        const int incl = ix_block_scan(tiles, scratch, &sum);
-        if (blockIdx.x == 0 && u < a.n_units) a.prefix[u] = (int)total + incl - tiles;
-        total += sum;
-    }
-    if (blockIdx.x == 0 && tid == 0) a.prefix[a.n_units] = (int)total;
-    const int sharers = q4_sharers(a.grid, a.min_tiles, total);
-    if ((int)blockIdx.x >= sharers || total == 0) return;
-    const long long begin = total * blockIdx.x / sharers, end = total * (blockIdx.x + 1) / sharers;
-    long long before = 0;
-    for (int u0 = 0; u0 < a.n_units; u0 += C::kThreads) {
-        const int u = u0 + tid;
-        const int tiles = u < a.n_units ? (q4_unit_len(p, u, false) + C::kTile - 1) / C::kTile : 0;
-        int sum;
-        const int incl = ix_block_scan(tiles, scratch, &sum);
-        const long long first = before + incl - tiles;
-        if (first <= begin && begin < first + tiles) {
-            scratch[40] = u;
-            scratch[41] = (int)(begin - first);
-        }
-        before += sum;
-        if (before > begin) break;
-    }
-    __syncthreads();
-    int unit = scratch[40], tile0 = scratch[41];
-    const uint8_t *cache = reinterpret_cast<const uint8_t *>(p.cache);
-    const long long max_pos = (long long)p.pt_stride * kPage;
-
+    const Q4Run run = q4_find_run<C::kTile>(p, a.n_units, a.grid, a.min_tiles, a.prefix, scratch);
+    int unit = run.unit, tile0 = run.tile;
     Q4Consumer w;
     w.init(warp, lane);
     int it = 0;
-    for (long long at = begin; at < end; ++unit, tile0 = 0) {
+    for (long long at = run.begin; at < run.end; ++unit, tile0 = 0) {
         const int len = q4_unit_len(p, unit, false);
-        const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), end - at);
+        const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;  // a unit that sees nothing
         at += tiles;
         const int b = unit / p.T, tok0 = (unit - b * p.T) * p.pack;
         const int nrows = min(p.pack, p.dense_t - tok0) * p.dense_h;
         const long long row0 = ((long long)b * p.dense_t + tok0) * p.dense_h;
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
-        // page of this unit's tile t, -1 where none is mapped
-        auto page_of = [&](int t) {
-            if ((long long)t * kPage >= max_pos) return -1;
-            const int pg = ld_input(pt_b + t);
-            return (pg >= 0 && (long long)pg < p.num_pages) ? pg : -1;
-        };
+        auto page_of = [&](int t) { return q4_page(pt_b, p.pt_stride, p.num_pages, t); };
         auto issue = [&](int i, int pg) {  // thread 0
-            uint64_t *bar = &full[i & 1];
-            if (pg < 0) {
-                mbar_arrive(bar);  // nothing to copy
-                return;
-            }
-            mbar_arrive_expect_tx(bar, (uint32_t)C::kStageBytes);
-            bulk_g2s(smem + C::kOffStage + (i & 1) * C::kStageBytes,
-                     cache + (size_t)pg * (kPage * kQ4RowBytes), (uint32_t)C::kStageBytes, bar);
+            q4_copy_page(p, pg, smem + C::kOffStage + (i & 1) * C::kStageBytes, &full[i & 1]);
         };
         fence_proxy_async_smem();
         __syncthreads();  // the previous piece is done with the ring and with Q
@@ -548,7 +583,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
             issue(it, page_of(tile0));
             if (tiles > 1) issue(it + 1, page_of(tile0 + 1));
         }
-        q4_stage_q(smem + C::kOffQ, p.q, row0, nrows);
+        q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, row0, nrows);
         // visible positions of this lane's two query rows
         int lim0 = 0, lim1 = 0;
         if (w.r < nrows)
@@ -576,8 +611,9 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
                 }
                 __syncthreads();
             }
-            float sc[2][4];
-            w.scores(sbase + C::kOffQ, tile, sc);
+            float sg[1][2][4];
+            q4_scores<1>(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sg);
+            float (&sc)[2][4] = sg[0];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
