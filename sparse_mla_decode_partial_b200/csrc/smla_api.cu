@@ -1404,14 +1404,44 @@ static_assert(smla::kEvictBuffers == SMLA_EVICT_MAX_CACHES, "caches per apply ca
 
 namespace {
 
-template <int HG>
-cudaError_t launch_weigh_rows(const smla::WeighOld &p, int grid, cudaStream_t st) {
-    using C = smla::WeighCfg<HG>;
-    const cudaError_t e = ensure_smem_attr(
-        reinterpret_cast<const void *>(&smla::smla_evict_weigh_kernel<HG>), C::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(smla::smla_evict_weigh_kernel<HG>, grid, 32 * smla::kWeighWarps,
-                            C::kSmemBytes, st, p);
+// 2-D bf16 tensor of `rows` rows of 576 values, read in boxes of 64 values x
+// box_rows rows with the 128-byte swizzle.
+smla_status encode_rows576(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) {
+        std::snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled unavailable");
+        return SMLA_ERR_CUDA;
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)smla::kD, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)smla::kRowBytes};
+    const cuuint32_t box[2] = {64u, box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed: %d", (int)r);
+        return SMLA_ERR_CUDA;
+    }
+    return SMLA_OK;
+}
+
+smla_status launch_weigh_bf16(smla::WeighParams &a, cudaStream_t st) {
+    using C = smla::WeighTcCfg;
+    const int rows = a.p.dense_t * a.p.dense_h, npad = std::min((rows + 15) / 16 * 16, C::kMaxRows);
+    CUtensorMap map_kv, map_q;
+    smla_status s = encode_rows576(&map_kv, a.p.cache, (uint64_t)a.p.num_pages * SMLA_PAGE_SIZE, 64u);
+    if (s != SMLA_OK) return s;
+    s = encode_rows576(&map_q, a.p.q, (uint64_t)a.p.B * rows, (uint32_t)npad);
+    if (s != SMLA_OK) return s;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_weigh_bf16_kernel), C::kSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const long long pages = a.p.B * (((long long)a.p.K + 63) / 64);
+    a.grid = (int)std::min<long long>(pages, current_device_sms());
+    a.min_tiles = 2;
+    e = launch_dependent(smla::smla_weigh_bf16_kernel, a.grid, C::kThreads, C::kSmemBytes, st, map_kv, map_q, a);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
 template <int G>
@@ -1440,41 +1470,18 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
         return SMLA_ERR_MISALIGNED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const long long rows = (long long)T * H;
-    cudaError_t e;
-    if (Q4) {
-        smla::WeighParams a{};
-        a.p = make_params(q, cache, num_pages, page_table, pt_stride, nullptr, B, 1, (int)rows, max_n, scale, 1);
-        a.p.seq_lens = seq_lens;
-        a.p.pack = a.p.dense_t = T;
-        a.p.dense_h = H;
-        a.lse = lse;
-        a.acc = acc;
-        if (B * ((max_n + 63ll) / 64) > INT_MAX) return SMLA_ERR_INVALID_ARG;
-        e = rows <= 16 ? launch_weigh_q4<1>(a, st) : rows <= 32 ? launch_weigh_q4<2>(a, st) : launch_weigh_q4<4>(a, st);
-        return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
-    }
-    smla::WeighOld p{};
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.cache = static_cast<const uint8_t *>(cache);
-    p.num_pages = num_pages;
-    p.page_table = page_table;
-    p.pt_stride = pt_stride;
-    p.seq_lens = seq_lens;
-    p.lse = lse;
-    p.B = B;
-    p.T = T;
-    p.H = H;
-    p.scale_log2 = scale * smla::kLog2e;
-    p.acc = acc;
-    p.max_n = max_n;
-    const long long tiles = ((long long)max_n + smla::kWeighTile - 1) / smla::kWeighTile;
-    const long long most = (tiles + smla::kWeighWarps - 1) / smla::kWeighWarps;
-    p.nchunk = (int)std::max<long long>(1, std::min<long long>(most, (2ll * current_device_sms() + B - 1) / B));
-    if ((long long)B * p.nchunk > INT_MAX) return SMLA_ERR_INVALID_ARG;
-    const int grid = B * p.nchunk;
-    e = rows <= 16   ? launch_weigh_rows<1>(p, grid, st)
-        : rows <= 32 ? launch_weigh_rows<2>(p, grid, st)
-                     : launch_weigh_rows<4>(p, grid, st);
+    if (B * ((max_n + 63ll) / 64) > INT_MAX) return SMLA_ERR_INVALID_ARG;
+    smla::WeighParams a{};
+    a.p = make_params(q, cache, num_pages, page_table, pt_stride, nullptr, B, 1, (int)rows, max_n, scale, 1);
+    a.p.seq_lens = seq_lens;
+    a.p.pack = a.p.dense_t = T;
+    a.p.dense_h = H;
+    a.lse = lse;
+    a.acc = acc;
+    if (!Q4) return launch_weigh_bf16(a, st);
+    const cudaError_t e = rows <= 16   ? launch_weigh_q4<1>(a, st)
+                          : rows <= 32 ? launch_weigh_q4<2>(a, st)
+                                       : launch_weigh_q4<4>(a, st);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 

@@ -154,169 +154,207 @@ __global__ void __launch_bounds__(WeighQ4Cfg<G>::kThreads, WeighQ4Cfg<G>::kMinBl
 }
 
 // ---------------------------------------------------------------- bf16 rows
-struct WeighOld {
-    const __nv_bfloat16 *q;   // [B, T, H, 576]
-    const uint8_t *cache;     // bf16 rows of 1152 bytes
-    long long num_pages;
-    const int *page_table;    // [B, pt_stride]
-    int pt_stride;
-    const int *seq_lens;      // [B, T]
-    const float *lse;         // [B, T, H]
-    int B, T, H;
-    float scale_log2;
-    float *acc;               // [B, max_n]
-    int max_n;
-    int nchunk;               // CTAs per sequence
-};
-
-constexpr int kWeighWarps = 8;
-constexpr int kWeighTile = 32;  // cache rows per warp and step
-
-template <int HG>
-struct WeighCfg {
-    static constexpr int kRows = 16 * HG;  // query rows per pass
-    static constexpr int kOffFrag = 0;     // uint4 [36][HG][32]: A fragments in lane order
-    static constexpr int kOffLse = 36 * HG * 512;       // float2 [kRows]: lse in log2 units, high and low part
-    static constexpr int kOffLim = kOffLse + kRows * 8;  // int [kRows]: visible positions
-    static constexpr int kSmemBytes = kOffLim + kRows * 4;
-};
-
-// First of the four dims that lane column c feeds to k16 step s (dims +0, +1
-// go to k = 2 c, 2 c + 1 and dims +2, +3 to k = 2 c + 8, 2 c + 9).  The sum
-// over k does not care for the order of the dims, so each lane takes dims it
-// can load as 16 consecutive bytes: 8 bf16 values (two steps) or one whole
-// group of 32 codes (eight steps, one scale).
-__device__ __forceinline__ int weigh_dim(int s, int c) { return 32 * (s >> 1) + 8 * c + 4 * (s & 1); }
-
-// One warp: the scores of 32 cache rows (half a page, consecutive rows)
-// against 16 HG query rows by mma.sync, the cache rows (N) straight from
-// global memory into B fragments, the query rows (M) from shared memory.
-template <int HG>
-__device__ __forceinline__ void weigh_scores(const uint8_t *row0, const uint4 *frag, int lane,
-                                             float (&s)[HG][4][4]) {
-    const int c = lane & 3;
-    constexpr int kRow = kRowBytes;
-    const uint8_t *mine = row0 + (lane >> 2) * kRow;
-#pragma unroll
-    for (int g = 0; g < HG; ++g)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) s[g][n][0] = s[g][n][1] = s[g][n][2] = s[g][n][3] = 0.f;
-    auto step = [&](int st, const uint32_t (&b0)[4], const uint32_t (&b1)[4]) {
-#pragma unroll
-        for (int g = 0; g < HG; ++g) {
-            const uint4 a = frag[(st * HG + g) * 32 + lane];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mma_bf16_16816(s[g][n], a.x, a.y, a.z, a.w, b0[n], b1[n]);
-        }
-    };
-    auto chunk = [&](int st, const uint4 (&v)[4]) {  // 8 bf16 values per lane: two k16 steps
-        const uint32_t x[4] = {v[0].x, v[1].x, v[2].x, v[3].x}, y[4] = {v[0].y, v[1].y, v[2].y, v[3].y};
-        const uint32_t z[4] = {v[0].z, v[1].z, v[2].z, v[3].z}, w[4] = {v[0].w, v[1].w, v[2].w, v[3].w};
-        step(st, x, y);
-        step(st + 1, z, w);
-    };
-    {
-#pragma unroll 1
-        for (int j = 0; j < 18; j += 3) {
-            uint4 v[3][4];
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) v[k][n] = ld_row16(mine + n * 8 * kRow + 64 * (j + k) + 16 * c);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) chunk(2 * (j + k), v[k]);
-        }
+// 1152 bytes a row leave the tensor core about 50 cycles per row and SM, so the
+// rows go through tcgen05 with up to 128 query rows at once, the indexer's way:
+// the CACHE ROWS are M = 128 (two pages, each a column of TMA boxes of 64 rows x
+// 64 values, 128B swizzle), the query rows N, and the accumulator holds one
+// position per TMEM lane: the epilogue thread that owns a position adds up its
+// columns alone.  A CTA (one per SM) takes an equal run of the batch's pages.
+// Warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warps 4-7 epilogue.
+struct WeighTcCfg {
+    static constexpr int kThreads = 256;
+    static constexpr int kMaxRows = 128;                  // query rows per pass (the MMA's N)
+    static constexpr int kBoxBytes = 2 * 64 * 128;        // 128 cache rows x 64 values
+    static constexpr int kMaxStages = 12;
+    static constexpr int kTmemCols = 2 * kMaxRows;        // two accumulators
+    // full[], empty[], q_full, q_empty, acc_full[2], acc_empty[2]
+    static constexpr int kNumBars = 2 * kMaxStages + 6;
+    static constexpr int kOffRow = 0;                     // float4 [kMaxRows]: lse (two parts), visible positions
+    static constexpr int kOffBar = kOffRow + 16 * kMaxRows;
+    static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
+    static constexpr int kOffScratch = kOffTmem + 16;     // int [48]
+    static constexpr int kOffQ = (kOffScratch + 192 + 1023) / 1024 * 1024;  // [9][npad rows x 128 B], then the ring
+    static constexpr int kSmemBytes = 232448;
+    __host__ __device__ static constexpr int stages(int npad) {
+        const int n = (kSmemBytes - 1024 - kOffQ - npad * kRowBytes) / kBoxBytes;
+        return n < kMaxStages ? n : kMaxStages;
     }
-}
+};
+static_assert(WeighTcCfg::stages(128) >= 4, "ring of boxes");
 
-template <int HG>
-__global__ void __launch_bounds__(32 * kWeighWarps) smla_evict_weigh_kernel(const WeighOld p) {
-    using C = WeighCfg<HG>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint4 *frag = reinterpret_cast<uint4 *>(smem + C::kOffFrag);
-    float2 *lse_s = reinterpret_cast<float2 *>(smem + C::kOffLse);
-    int *lim_s = reinterpret_cast<int *>(smem + C::kOffLim);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
-    const int b = blockIdx.x / p.nchunk, part = blockIdx.x % p.nchunk;
+__global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
+    smla_weigh_bf16_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
+                           const WeighParams a) {
+    using C = WeighTcCfg;
+    const PartialParams &p = a.p;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.dense_t * p.dense_h;
+    const int npad = min((rows + 15) / 16 * 16, C::kMaxRows);
+    const int nst = C::stages(npad);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kMaxStages;
+    uint64_t *q_full = empty + C::kMaxStages, *q_empty = q_full + 1;
+    uint64_t *acc_full = q_empty + 1, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t q_addr = sbase + C::kOffQ, ring = q_addr + npad * kRowBytes;
+    bool dead = false;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kMaxStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 128);
+        }
+        fence_mbar_init();
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    int len = 0;  // longest visible length of the sequence's query tokens
-    for (int t = 0; t < p.T; ++t) {
-        const int raw = ld_input(p.seq_lens + (size_t)b * p.T + t);
-        len = max(len, min(max(raw, 0), p.max_n));
-        if (part == 0 && threadIdx.x == t % blockDim.x && (raw < 0 || raw > p.max_n)) count_bad_index();
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
     }
-    const int tiles = (len + kWeighTile - 1) / kWeighTile;
-    const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
-    const int rows = p.T * p.H;
-    constexpr int kRow = kRowBytes;
+    const Q4Run run = q4_find_run<64>(p, p.B, a.grid, a.min_tiles, nullptr,
+                                      reinterpret_cast<int *>(smem + C::kOffScratch));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
-    for (int g0 = 0; g0 < rows; g0 += C::kRows) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 36 * HG * 32; i += blockDim.x) {
-            const int l = i & 31, g = (i >> 5) % HG, st = i / (32 * HG);
-            const int r = g0 + 16 * g + (l >> 2), d = weigh_dim(st, l & 3);
-            const __nv_bfloat16 *q = p.q + ((size_t)b * rows + r) * kD + d;
-            uint2 lo = make_uint2(0u, 0u), hi = lo;
-            if (r < rows) lo = *reinterpret_cast<const uint2 *>(q);
-            if (r + 8 < rows) hi = *reinterpret_cast<const uint2 *>(q + 8 * kD);
-            frag[i] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+    // Every role walks the same pieces (a run of one sequence's pages), passes
+    // (of kMaxRows query rows) and steps (of two pages).
+    auto walk = [&](auto &&body) {
+        int b = run.unit, page0 = run.tile;
+        for (long long at = run.begin; at < run.end; ++b, page0 = 0) {
+            const int len = q4_unit_len(p, b, false);
+            const int pages = (int)min((long long)((len + 63) / 64 - page0), run.end - at);
+            if (pages <= 0) continue;
+            at += pages;
+            for (int g0 = 0; g0 < rows; g0 += C::kMaxRows) body(b, len, page0, pages, g0);
         }
-        for (int i = threadIdx.x; i < C::kRows; i += blockDim.x) {
-            const int r = g0 + i;
-            float2 l2 = make_float2(0.f, 0.f);
-            int lim = 0;
-            if (r < rows) {
-                const float l = p.lse[(size_t)b * rows + r];
-                // lse in log2 units as a sum of two floats: its rounding would
-                // otherwise scale every weight of the row
-                const double x = (double)l * 1.4426950408889634074;
-                l2.x = (float)x;
-                l2.y = isfinite(l2.x) ? (float)(x - (double)l2.x) : 0.f;
-                // a row that attended to nothing (lse = -inf) gives no weight
-                lim = l == -INFINITY ? 0 : min(max(ld_input(p.seq_lens + (size_t)b * p.T + r / p.H), 0), p.max_n);
-            }
-            lse_s[i] = l2;
-            lim_s[i] = lim;
-        }
-        __syncthreads();
-        for (int tile = part * kWeighWarps + warp; tile < tiles; tile += p.nchunk * kWeighWarps) {
-            const int pos0 = tile * kWeighTile;
-            const long long row = paged_row(pt_b, p.pt_stride, p.num_pages, pos0);
-            if (row < 0) {
-                if (g0 == 0 && lane < min(kWeighTile, len - pos0)) count_bad_index();
-                continue;
-            }
-            float s[HG][4][4];
-            weigh_scores<HG>(p.cache + row * kRow, frag, lane, s);
-            float w[8];  // column 8 n + 2 c + e at [2 n + e]
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = 0.f;
-#pragma unroll
-            for (int g = 0; g < HG; ++g) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = 16 * g + 8 * h + (lane >> 2);
-                    const float2 l2 = lse_s[r];
-                    const int lim = lim_s[r] - pos0 - 2 * c;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float x = fmaf(s[g][k >> 1][2 * h + (k & 1)], p.scale_log2, -l2.x) - l2.y;
-                        w[k] += 8 * (k >> 1) + (k & 1) < lim ? fast_exp2(x) : 0.f;
+    };
+
+    if (warp == 0) {
+        // ============================================================ TMA producer
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+            int st = 0, round = 0, piece = 0;
+            walk([&](int b, int len, int page0, int pages, int g0) {
+                const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
+                if (piece > 0) mbar_wait(q_empty, (piece - 1) & 1, dead);
+                ++piece;
+                mbar_arrive_expect_tx(q_full, (uint32_t)(npad * kRowBytes));
+#pragma unroll 1
+                for (int k = 0; k < 9; ++k)
+                    tma_load_2d(q_addr + k * npad * 128, &map_q, 64 * k, b * rows + g0, q_full, keep);
+                for (int t = 0; t < pages; t += 2) {
+                    const int pg0 = q4_page(pt_b, p.pt_stride, p.num_pages, page0 + t);
+                    const int pg1 = t + 1 < pages ? q4_page(pt_b, p.pt_stride, p.num_pages, page0 + t + 1) : -1;
+                    const uint32_t bytes = (pg0 >= 0 ? 8192u : 0u) + (pg1 >= 0 ? 8192u : 0u);
+#pragma unroll 1
+                    for (int k = 0; k < 9; ++k) {
+                        if (round > 0) mbar_wait(&empty[st], (round - 1) & 1, dead);
+                        mbar_arrive_expect_tx(&full[st], bytes);
+                        const uint32_t dst = ring + st * C::kBoxBytes;
+                        if (pg0 >= 0) tma_load_2d(dst, &map_kv, 64 * k, pg0 * 64, &full[st], once);
+                        if (pg1 >= 0) tma_load_2d(dst + 8192, &map_kv, 64 * k, pg1 * 64, &full[st], once);
+                        if (++st == nst) {
+                            st = 0;
+                            ++round;
+                        }
                     }
                 }
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] += __shfl_xor_sync(0xffffffffu, w[k], o);
-            float v = w[0];
-#pragma unroll
-            for (int k = 1; k < 8; ++k) v = (lane >> 2) == k ? w[k] : v;
-            const int pos = pos0 + 8 * (lane >> 3) + 2 * c + ((lane >> 2) & 1);
-            if (pos < len) p.acc[(size_t)b * p.max_n + pos] += v;
+            });
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ============================================================ MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(128, npad, false, false);
+            int st = 0, round = 0, piece = 0, step = 0;
+            walk([&](int, int, int, int pages, int) {
+                mbar_wait(q_full, piece & 1, dead);
+                ++piece;
+                for (int t = 0; t < pages; t += 2, ++step) {
+                    const int acc = step & 1;
+                    if (step >= 2) mbar_wait(&acc_empty[acc], ((step >> 1) - 1) & 1, dead);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 9; ++k) {
+                        mbar_wait(&full[st], round & 1, dead);
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc(ring + st * C::kBoxBytes, 16, 1024, kSwizzle128B);
+                        const uint64_t bd = smem_desc(q_addr + k * npad * 128, 16, 1024, kSwizzle128B);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(tmem + acc * C::kMaxRows, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) ? 1u : 0u);
+                        umma_commit(&empty[st]);
+                        if (++st == nst) {
+                            st = 0;
+                            ++round;
+                        }
+                    }
+                    umma_commit(&acc_full[acc]);
+                }
+                umma_commit(q_empty);
+            });
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ============================================================ epilogue
+        const int row = threadIdx.x - 128;  // TMEM lane: cache row of the step's two pages
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float4 *row_s = reinterpret_cast<float4 *>(smem + C::kOffRow);
+        int step = 0;
+        walk([&](int b, int len, int page0, int pages, int g0) {
+            named_bar_sync(1, 128);  // the previous pass is done with row_s
+            {
+                float2 l2;
+                int lim;
+                weigh_row(a, b, g0 + row, &l2, &lim);
+                row_s[row] = make_float4(l2.x, l2.y, __int_as_float(lim), 0.f);
+            }
+            named_bar_sync(1, 128);
+            const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
+            float *acc_b = a.acc + (size_t)b * p.K;
+            for (int t = 0; t < pages; t += 2, ++step) {
+                const int page = page0 + t + (row >> 6), pos = page * 64 + (row & 63);
+                const bool mine = page < page0 + pages && pos < len;
+                const bool mapped = mine && q4_page(pt_b, p.pt_stride, p.num_pages, page) >= 0;
+                if (mine && !mapped && g0 == 0) count_bad_index();
+                float sum = 0.f;
+                if (mapped) asm volatile("ld.global.f32 %0, [%1];" : "=f"(sum) : "l"(acc_b + pos));
+                mbar_wait(&acc_full[step & 1], (step >> 1) & 1, dead);
+                tc_fence_after();
+                float w = 0.f;
+#pragma unroll 1
+                for (int n = 0; n < npad; n += 16) {
+                    uint32_t s[16];
+                    tmem_ld_cols<16>(t_lane + (step & 1) * C::kMaxRows + n, s);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float4 q = row_s[n + k];
+                        const float x = fmaf(__uint_as_float(s[k]), p.scale_log2, -q.x) - q.y;
+                        w += pos < __float_as_int(q.z) ? fast_exp2(x) : 0.f;
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&acc_empty[step & 1]);
+                if (mapped) acc_b[pos] = sum + w;
+            }
+        });
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
     }
 }
 
