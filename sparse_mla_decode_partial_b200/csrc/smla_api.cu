@@ -1209,7 +1209,9 @@ Q4Dense q4_dense(int B, int T, int H, int nsplit) {
     d.units = (T + most - 1) / most;
     d.pack = (T + d.units - 1) / d.units;
     d.n_units = (long long)B * d.units;
-    d.ctas = d.n_units * nsplit;
+    // nsplit CTAs per unit, but no more than run at once
+    const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();
+    d.ctas = std::min(d.n_units * nsplit, std::max(slots, d.n_units));
     const size_t rows = (size_t)(d.ctas + d.n_units) * kQ4Rows;
     d.off_ml = round256(rows * smla::kDc * sizeof(float));
     d.off_prefix = d.off_ml + round256(rows * sizeof(float2));
@@ -1317,7 +1319,7 @@ int smla_dense_q4_nsplit(int B, int T, int H, int K) {
     // one full wave of CTAs
     const long long n = (long long)B * q4_dense(B, T, H, 1).units;
     const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();
-    return (int)std::max<long long>(1, std::min<long long>(SMLA_MAX_NSPLIT, slots / n));
+    return (int)std::max<long long>(1, std::min<long long>(SMLA_MAX_NSPLIT, (slots + n - 1) / n));
 }
 
 size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {

@@ -134,10 +134,16 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
     const int c = lane & 3;
     const uint32_t row = rows + q4_row_of(lane >> 2) * kQ4RowBytes;
     q += 16 * lane;
+    // With one group, even and odd steps keep accumulators of their own: two
+    // chains of 36 dependent products left the pipe waiting for their latency.
+    constexpr int kOdd = G == 1 ? 1 : 0;
+    float odd[2][4];
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int i = 0; i < 2; ++i) {
+        odd[i][0] = odd[i][1] = odd[i][2] = odd[i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s[g][i][0] = s[g][i][1] = s[g][i][2] = s[g][i][3] = 0.f;
+        for (int g = 0; g < G; ++g) s[g][i][0] = s[g][i][1] = s[g][i][2] = s[g][i][3] = 0.f;
+    }
     auto steps = [&](int st, const uint4 (&v)[2]) {  // k16 steps st, st + 1
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -145,7 +151,7 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 mma_bf16_16816(s[g][i], a0.x, a0.y, a0.z, a0.w, v[i].x, v[i].y);
-                mma_bf16_16816(s[g][i], a1.x, a1.y, a1.z, a1.w, v[i].z, v[i].w);
+                mma_bf16_16816(kOdd ? odd[i] : s[g][i], a1.x, a1.y, a1.z, a1.w, v[i].z, v[i].w);
             }
         }
     };
@@ -176,6 +182,12 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
 #pragma unroll
         for (int i = 0; i < 2; ++i) v[i] = lds_16(row + i * 8 * kQ4RowBytes + kQ4OffRope + 64 * j + 16 * c);
         steps(32 + 2 * j, v);
+    }
+    if (kOdd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[0][i][k] += odd[i][k];
     }
 }
 
