@@ -497,13 +497,14 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
  * conventions, clamping and errors.  o is rounded to bf16 once per output (and
  * each probability once, as in the bf16 decode); the decoded latents are exact.
  *   nsplit  0 picks smla_q4_nsplit(B, T, H, K), smla_dense_q4_nsplit(B, T, H, K)
- *   workspace_bytes  at least smla_workspace_bytes(B, T, H, nsplit) (nothing
- *           for nsplit 1), or smla_dense_q4_workspace_bytes(B, T, H, K, nsplit),
- *           for the nsplit used; else SMLA_ERR_WORKSPACE_TOO_SMALL
+ *   workspace_bytes  at least smla_q4_workspace_bytes(B, T, H, K, nsplit), or
+ *           smla_dense_q4_workspace_bytes(B, T, H, K, nsplit), with the nsplit
+ *           of the call (0 included); else SMLA_ERR_WORKSPACE_TOO_SMALL
  * K above SMLA_MAX_K gives SMLA_ERR_INVALID_ARG.  Calls that may overlap on the
  * GPU, two captured graphs among them, need a workspace each.
  */
 int smla_q4_nsplit(int B, int T, int H, int K);
+size_t smla_q4_workspace_bytes(int B, int T, int H, int K, int nsplit);
 smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_pages,
                            const int32_t *page_table, int pt_stride, const int32_t *topk_idx, int B,
                            int T, int H, int K, int page_size, float scale, int nsplit, void *workspace,
@@ -553,8 +554,9 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  *           carried along (slot i from src[b, i]); 0 and -1 from m on.
  *    acc_new, pos_new and n_new must not overlap acc, pos and n
  *    (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
- *    outside [0, max_n] is clamped and counted.  workspace: device, 16-B
- *    aligned, at least smla_evict_workspace_bytes(B, max_n).
+ *    outside [0, max_n] is clamped and counted.  workspace is used only where
+ *    pos_new is NULL (it may be NULL otherwise): device, 16-B aligned, at least
+ *    smla_evict_workspace_bytes(B, max_n).
  *
  * 3. smla_evict_apply moves the rows, in place, in up to SMLA_EVICT_MAX_CACHES
  *    paged buffers that share the page table: for every i with src[b, i] not

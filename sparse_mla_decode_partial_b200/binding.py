@@ -63,6 +63,7 @@ SIGNATURES = {
     "smla_q4_append": (_I, [_P, _I, _P, _P, _I, _P, _I64, _P, _I, _I, _P]),
     "smla_q4_read": (_I, [_P, _I64, _P, _I, _P, _I, _I, _I, _P, _P]),
     "smla_q4_nsplit": (_I, [_I, _I, _I, _I]),
+    "smla_q4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "smla_decode_q4": (_I, [_P, _P, _I64, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _P,
                             _P]),
     "smla_dense_q4_nsplit": (_I, [_I, _I, _I, _I]),
@@ -504,10 +505,12 @@ def _launch(name, dev, stream, *args):
 
 def _want(t, dtype, name, device, shape=None):
     """_need() for a tensor that must be on ``device``, with the checks that pass
-    in one expression; what fails is left to _need to name."""
+    in one expression (a CPU tensor's get_device() is -1); what fails is left to
+    _need to name."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
-            and (shape is None or t.shape == shape) and t.is_cuda and t.get_device() == device.index):
+            and (shape is None or t.shape == shape) and t.get_device() == device.index):
         _need(t, dtype, name, device, shape)
+        _on_device(t, name, device)
 
 
 def _new(shape, dtype, dev, stream):
@@ -522,18 +525,29 @@ def _new(shape, dtype, dev, stream):
     return t
 
 
-def _pages_of(cache, width, what):
-    """Number of pages of a paged cache tensor [num_pages, 64, width]."""
-    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or cache.shape[2] != width:
-        raise ValueError(f"{what} must be [num_pages, {PAGE_SIZE}, {width}], got {list(cache.shape)}")
-    return cache.shape[0]
+def _paged(cache, width, dtype, dev, page_table, B):
+    """Pages of a paged cache [num_pages, 64, width], and the page table's width."""
+    _want(cache, dtype, "cache", dev)
+    shape = cache.shape
+    if len(shape) != 3 or shape[1] != PAGE_SIZE or shape[2] != width:
+        raise ValueError(f"cache must be [num_pages, {PAGE_SIZE}, {width}], got {list(shape)}")
+    return shape[0], _table(page_table, B, dev)
 
 
-def _table(page_table, B, device):
-    _want(page_table, torch.int32, "page_table", device)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+def _table(page_table, B, dev):
+    _want(page_table, torch.int32, "page_table", dev)
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("page_table must be [B, pt_stride]")
-    return page_table.shape[1]
+    return shape[1]
+
+
+def _dims(t, n, what):
+    """Shape of a tensor of n dimensions."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(what)
+    return shape
 
 
 def q4_append(rows, cache, page_table, cu_rows, start, *, stream=None):
@@ -544,18 +558,15 @@ def q4_append(rows, cache, page_table, cu_rows, start, *, stream=None):
     left out.  Writes into cache and returns it."""
     _need(rows, torch.bfloat16, "rows")
     dev = rows.device
-    if rows.dim() != 2 or rows.shape[1] != D:
+    n, width = _dims(rows, 2, f"rows must be [N, {D}]")
+    if width != D:
         raise ValueError(f"rows must be [N, {D}]")
     _want(start, torch.int32, "start", dev)
-    if start.dim() != 1:
-        raise ValueError("start must be [B]")
-    B = start.shape[0]
+    B, = _dims(start, 1, "start must be [B]")
     _want(cu_rows, torch.int32, "cu_rows", dev, (B + 1,))
-    _want(cache, torch.uint8, "cache", dev)
-    num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
-    pt_stride = _table(page_table, B, dev)
-    _launch("smla_q4_append", dev, stream, _ptr(rows), _k_in_range(rows.shape[0]), _ptr(cu_rows),
-            _ptr(start), B, _ptr(cache), num_pages, _ptr(page_table), pt_stride, PAGE_SIZE)
+    num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
+    _launch("smla_q4_append", dev, stream, rows.data_ptr(), _k_in_range(n), cu_rows.data_ptr(),
+            start.data_ptr(), B, cache.data_ptr(), num_pages, page_table.data_ptr(), pt_stride, PAGE_SIZE)
     return cache
 
 
@@ -564,17 +575,15 @@ def q4_read(cache, page_table, positions, *, out=None, stream=None):
     positions[b, j] of sequence b (int32 [B, K]; -1 gives zeros)."""
     _need(cache, torch.uint8, "cache")
     dev = cache.device
-    num_pages = _pages_of(cache, Q4_ROW_BYTES, "cache")
     _want(positions, torch.int32, "positions", dev)
-    if positions.dim() != 2:
-        raise ValueError("positions must be [B, K]")
-    B, K = positions.shape
-    pt_stride = _table(page_table, B, dev)
+    B, K = _dims(positions, 2, "positions must be [B, K]")
+    num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
     if out is None:
         out = _new((B, K, D), torch.bfloat16, dev, stream)
-    _want(out, torch.bfloat16, "out", dev, (B, K, D))
-    _launch("smla_q4_read", dev, stream, _ptr(cache), num_pages, _ptr(page_table), pt_stride,
-            _ptr(positions), B, _k_in_range(K), PAGE_SIZE, _ptr(out))
+    else:
+        _want(out, torch.bfloat16, "out", dev, (B, K, D))
+    _launch("smla_q4_read", dev, stream, cache.data_ptr(), num_pages, page_table.data_ptr(), pt_stride,
+            positions.data_ptr(), B, _k_in_range(K), PAGE_SIZE, out.data_ptr())
     return out
 
 
@@ -582,22 +591,25 @@ def q4_nsplit(B: int, T: int, H: int, K: int) -> int:
     return int(lib().smla_q4_nsplit(B, T, H, _k_in_range(K)))
 
 
+def q4_workspace_bytes(B: int, T: int, H: int, K: int, nsplit: int = 0) -> int:
+    return int(lib().smla_q4_workspace_bytes(B, T, H, _k_in_range(K), nsplit))
+
+
 def dense_q4_nsplit(B: int, T: int, H: int, K: int) -> int:
     return int(lib().smla_dense_q4_nsplit(B, T, H, _k_in_range(K)))
 
 
-def dense_q4_workspace_bytes(B: int, T: int, H: int, K: int, nsplit: int) -> int:
+def dense_q4_workspace_bytes(B: int, T: int, H: int, K: int, nsplit: int = 0) -> int:
     return int(lib().smla_dense_q4_workspace_bytes(B, T, H, _k_in_range(K), nsplit))
 
 
-def _q4_decode_args(q, cache, page_table):
+def _queries(q):
+    """Device and [B, T, H] of a decode's queries."""
     _need(q, torch.bfloat16, "q")
-    dev = q.device
-    if q.dim() != 4 or q.shape[-1] != D:
+    B, T, H, width = _dims(q, 4, f"q must be [B,T,H,{D}]")
+    if width != D:
         raise ValueError(f"q must be [B,T,H,{D}]")
-    B, T, H, _ = q.shape
-    _want(cache, torch.uint8, "cache", dev)
-    return dev, B, T, H, _pages_of(cache, Q4_ROW_BYTES, "cache"), _table(page_table, B, dev)
+    return q.device, B, T, H
 
 
 def _decode_out(dev, B, T, H, need, workspace, o, lse, stream):
@@ -621,18 +633,17 @@ def decode_q4(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, works
               lse=None, stream=None):
     """decode() over a 4-bit cache (uint8 [num_pages, 64, 416], as q4_append
     writes it); returns (o bf16 [B,T,H,512], lse fp32 [B,T,H])."""
-    dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
+    dev, B, T, H = _queries(q)
+    num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
     _want(idx, torch.int32, "idx", dev)
-    if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, T):
+    b, t, K = _dims(idx, 3, "idx must be [B,T,K]")
+    if b != B or t != T:
         raise ValueError("idx must be [B,T,K]")
-    K = _k_in_range(idx.shape[2])
-    if nsplit == 0:
-        nsplit = q4_nsplit(B, T, H, K)
-    need = workspace_bytes(B, T, H, nsplit) if nsplit > 1 else 0
+    need = q4_workspace_bytes(B, T, H, K, nsplit) if workspace is None else 0
     workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
-    _launch("smla_decode_q4", dev, stream, _ptr(q), _ptr(cache), num_pages, _ptr(page_table),
-            pt_stride, _ptr(idx), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit), _ptr(workspace),
-            workspace.numel(), _ptr(o), _ptr(lse))
+    _launch("smla_decode_q4", dev, stream, q.data_ptr(), cache.data_ptr(), num_pages, page_table.data_ptr(),
+            pt_stride, idx.data_ptr(), B, T, H, _k_in_range(K), PAGE_SIZE, scale, nsplit,
+            workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
     return o, lse
 
 
@@ -641,20 +652,17 @@ def decode_dense_q4(q, cache, page_table, seq_lens, scale: float, nsplit: int = 
     """decode_dense() over a 4-bit cache: query token (b, t) attends to
     positions 0 .. seq_lens[b, t] - 1 of sequence b.  K defaults to the longest
     length (read from seq_lens, which synchronises)."""
-    dev, B, T, H, num_pages, pt_stride = _q4_decode_args(q, cache, page_table)
-    _want(seq_lens, torch.int32, "seq_lens", dev)
-    if tuple(seq_lens.shape) != (B, T):
-        raise ValueError("seq_lens must be [B,T]")
+    dev, B, T, H = _queries(q)
+    num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
+    _want(seq_lens, torch.int32, "seq_lens", dev, (B, T))
     if K is None:
         K = int(seq_lens.max().item()) if seq_lens.numel() else 0
     K = _k_in_range(int(K))
-    if nsplit == 0:
-        nsplit = dense_q4_nsplit(B, T, H, K)
-    need = dense_q4_workspace_bytes(B, T, H, K, nsplit)
+    need = dense_q4_workspace_bytes(B, T, H, K, nsplit) if workspace is None else 0
     workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
-    _launch("smla_decode_dense_q4", dev, stream, _ptr(q), _ptr(cache), num_pages, _ptr(page_table),
-            pt_stride, _ptr(seq_lens), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit),
-            _ptr(workspace), workspace.numel(), _ptr(o), _ptr(lse))
+    _launch("smla_decode_dense_q4", dev, stream, q.data_ptr(), cache.data_ptr(), num_pages,
+            page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), B, T, H, K, PAGE_SIZE, scale, nsplit,
+            workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
     return o, lse
 
 
@@ -681,28 +689,24 @@ def evict_accumulate(q, cache, page_table, seq_lens, lse, scale: float, acc, *, 
     query tokens of a dense decode gave to each position: q, seq_lens and lse
     are that decode's.  cache is the bf16 or the 4-bit latent cache.  Returns
     acc."""
-    _need(q, torch.bfloat16, "q")
-    dev = q.device
-    if q.dim() != 4 or q.shape[-1] != D:
-        raise ValueError(f"q must be [B,T,H,{D}]")
-    B, T, H, _ = q.shape
-    q4 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
-    _want(cache, torch.uint8 if q4 else torch.bfloat16, "cache", dev)
-    num_pages = _pages_of(cache, Q4_ROW_BYTES if q4 else D, "cache")
-    pt_stride = _table(page_table, B, dev)
+    dev, B, T, H = _queries(q)
+    q4 = isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8
+    num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES if q4 else D, torch.uint8 if q4 else torch.bfloat16, dev,
+                                  page_table, B)
     _want(seq_lens, torch.int32, "seq_lens", dev, (B, T))
     _want(lse, torch.float32, "lse", dev, (B, T, H))
     _want(acc, torch.float32, "acc", dev)
-    if acc.dim() != 2 or acc.shape[0] != B:
+    b, max_n = _dims(acc, 2, "acc must be [B, max_n]")
+    if b != B:
         raise ValueError("acc must be [B, max_n]")
-    _launch("smla_evict_accumulate_q4" if q4 else "smla_evict_accumulate", dev, stream, _ptr(q),
-            _ptr(cache), num_pages, _ptr(page_table), pt_stride, _ptr(seq_lens), _ptr(lse), B, T, H,
-            PAGE_SIZE, float(scale), _ptr(acc), _k_in_range(acc.shape[1]))
+    _launch("smla_evict_accumulate_q4" if q4 else "smla_evict_accumulate", dev, stream, q.data_ptr(),
+            cache.data_ptr(), num_pages, page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), lse.data_ptr(),
+            B, T, H, PAGE_SIZE, scale, acc.data_ptr(), _k_in_range(max_n))
     return acc
 
 
 def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, src=None, n_new=None,
-               acc_new=None, pos_new=None, workspace=None, stream=None) -> EvictPlan:
+               acc_new=None, pos_new=None, stream=None) -> EvictPlan:
     """Choose the min(n[b], K) slots of each sequence that stay, by accumulated
     weight acc (fp32 [B, max_n]), and which row each slot takes.  pos (int32
     [B, max_n], default: the slot's number) is the token's original position:
@@ -710,32 +714,32 @@ def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, 
     carried along to the new slots; the inputs are left as they are."""
     _need(acc, torch.float32, "acc")
     dev = acc.device
-    if acc.dim() != 2:
-        raise ValueError("acc must be [B, max_n]")
-    B, max_n = acc.shape
+    B, max_n = _dims(acc, 2, "acc must be [B, max_n]")
     K = _k_in_range(int(K))
     if K < 1:
         raise ValueError("K must be at least 1")
     _want(n, torch.int32, "n", dev, (B,))
     if pos is not None:
         _want(pos, torch.int32, "pos", dev, (B, max_n))
-    outs = []
-    for t, name, dtype, shape in ((src, "src", torch.int32, (B, K)), (n_new, "n_new", torch.int32, (B,)),
-                                  (acc_new, "acc_new", torch.float32, (B, max_n)),
-                                  (pos_new, "pos_new", torch.int32, (B, max_n))):
-        if t is None:
-            t = _new(shape, dtype, dev, stream)
-        else:
-            _want(t, dtype, name, dev, shape)
-        outs.append(t)
-    src, n_new, acc_new, pos_new = outs
-    if workspace is None:
-        workspace = _new(max(16, evict_workspace_bytes(B, max_n)), torch.uint8, dev, stream)
+    if src is None:
+        src = _new((B, K), torch.int32, dev, stream)
     else:
-        _want(workspace, torch.uint8, "workspace", dev)
-    _launch("smla_evict_plan", dev, stream, _ptr(acc), _ptr(pos), _ptr(n), B, max_n, K, int(n_sink),
-            int(n_recent), _ptr(workspace), workspace.numel(), _ptr(src), _ptr(n_new),
-            _ptr(acc_new), _ptr(pos_new))
+        _want(src, torch.int32, "src", dev, (B, K))
+    if n_new is None:
+        n_new = _new((B,), torch.int32, dev, stream)
+    else:
+        _want(n_new, torch.int32, "n_new", dev, (B,))
+    if acc_new is None:
+        acc_new = _new((B, max_n), torch.float32, dev, stream)
+    else:
+        _want(acc_new, torch.float32, "acc_new", dev, (B, max_n))
+    if pos_new is None:
+        pos_new = _new((B, max_n), torch.int32, dev, stream)
+    else:
+        _want(pos_new, torch.int32, "pos_new", dev, (B, max_n))
+    _launch("smla_evict_plan", dev, stream, acc.data_ptr(), None if pos is None else pos.data_ptr(),
+            n.data_ptr(), B, max_n, K, n_sink, n_recent, None, 0, src.data_ptr(), n_new.data_ptr(),
+            acc_new.data_ptr(), pos_new.data_ptr())
     return EvictPlan(src, n_new, acc_new, pos_new)
 
 
@@ -746,23 +750,24 @@ def evict_apply(src, page_table, caches, *, stream=None):
     cache, the index keys.  Returns caches."""
     _need(src, torch.int32, "src")
     dev = src.device
-    if src.dim() != 2:
-        raise ValueError("src must be [B, K]")
-    B, K = src.shape
+    B, K = _dims(src, 2, "src must be [B, K]")
     pt_stride = _table(page_table, B, dev)
     if not 1 <= len(caches) <= EVICT_MAX_CACHES:
         raise ValueError(f"caches must be 1 to {EVICT_MAX_CACHES} tensors")
-    ptrs, sizes, num_pages = (_P * len(caches))(), (ctypes.c_int32 * len(caches))(), None
-    for k, t in enumerate(caches):
+    ptrs, sizes, num_pages = [], [], None
+    for t in caches:
         if not isinstance(t, torch.Tensor):
             raise TypeError("caches must be torch.Tensors")
-        _need(t, t.dtype, f"caches[{k}]", dev)
-        if t.dim() != 3 or t.shape[1] != PAGE_SIZE or t.shape[0] != caches[0].shape[0]:
-            raise ValueError(f"caches[{k}] must be [num_pages, {PAGE_SIZE}, width], the same pages in all")
-        num_pages, ptrs[k], sizes[k] = t.shape[0], t.data_ptr(), t.shape[2] * t.element_size()
-    _check(lib().smla_evict_apply(_ptr(src), B, _k_in_range(K), _ptr(page_table), pt_stride, num_pages,
-                                  PAGE_SIZE, ptrs, sizes, len(caches), _stream(stream)),
-           "smla_evict_apply")
+        _want(t, t.dtype, "a cache", dev)
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != PAGE_SIZE or num_pages not in (None, shape[0]):
+            raise ValueError(f"caches must be [num_pages, {PAGE_SIZE}, width], the same pages in all")
+        num_pages = shape[0]
+        ptrs.append(t.data_ptr())
+        sizes.append(shape[2] * t.element_size())
+    n = len(ptrs)
+    _launch("smla_evict_apply", dev, stream, src.data_ptr(), B, _k_in_range(K), page_table.data_ptr(), pt_stride,
+            num_pages, PAGE_SIZE, (_P * n)(*ptrs), (ctypes.c_int32 * n)(*sizes), n)
     return caches
 
 

@@ -1195,6 +1195,28 @@ smla_status launch_q4_sparse(const PartialParams &p, int grid, cudaStream_t st) 
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
+// Splits of an index list over the 4-bit cache, up to 16 heads.  Measured: a
+// CTA alone on its SM takes 1.36 times as long per 64-row tile as an SM with two
+// or more needs per tile, and a further CTA costs about one tile (list, first
+// rows, partials).  So the cost of S splits, in tiles, is
+//   ceil(tiles / S) * max(1.36, r) + r,   r = CTAs per SM.
+// (64 lists of 2048: S = 2, 4, 8 cost 21.8 + 1, 18, 20 and took 44, 37, 43 us.)
+int q4_sparse_nsplit(long long bt, int K, int sms) {
+    const int tiles = (K + smla::Q4Cfg::kTile - 1) / smla::Q4Cfg::kTile;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= tiles && s <= SMLA_MAX_NSPLIT; ++s) {
+        const double r = (double)((bt * s + sms - 1) / sms);
+        const double cost = ((tiles + s - 1) / s) * std::max(1.36, r) + r;
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = s;
+        }
+        if (r > 8.0) break;  // more CTAs per SM only add to the cost from here
+    }
+    return best;
+}
+
 // The dense schedule over packed units of at most kQ4Rows query rows.
 constexpr int kQ4MinTiles = 2;
 bool q4_dense_small(int T, int H) { return (long long)T * H <= kQ4Rows; }
@@ -1279,7 +1301,13 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
 int smla_q4_nsplit(int B, int T, int H, int K) {
     if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
     if (H > kQ4Rows) return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
-    return smla_choose_nsplit(B, T, H, K, 0);
+    return q4_sparse_nsplit((long long)B * T, K, current_device_sms());
+}
+
+size_t smla_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {
+    if (B < 0 || T < 0 || H < 0 || K < 0 || nsplit < 0 || nsplit > SMLA_MAX_NSPLIT) return 0;
+    if (nsplit == 0) nsplit = smla_q4_nsplit(B, T, H, K);
+    return nsplit > 1 ? smla_workspace_bytes(B, T, H, nsplit) : 0;
 }
 
 smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_pages,
@@ -1304,7 +1332,7 @@ smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_page
         p.lse = lse;
         return launch_q4_sparse<true>(p, (int)grid, s);
     }
-    if (workspace_bytes < smla_workspace_bytes(B, T, H, nsplit)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < smla_q4_workspace_bytes(B, T, H, K, nsplit)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
     if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
     set_partials(&p, workspace, (size_t)B * T * H * nsplit);
@@ -1323,7 +1351,8 @@ int smla_dense_q4_nsplit(int B, int T, int H, int K) {
 }
 
 size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {
-    if (B < 0 || T < 0 || H < 0 || K < 0 || nsplit < 1 || nsplit > SMLA_MAX_NSPLIT) return 0;
+    if (B < 0 || T < 0 || H < 0 || K < 0 || nsplit < 0 || nsplit > SMLA_MAX_NSPLIT) return 0;
+    if (nsplit == 0) nsplit = smla_dense_q4_nsplit(B, T, H, K);
     if (q4_dense_small(T, H)) return q4_dense(B, T, H, nsplit).bytes;
     return smla_dense_workspace_bytes(B, T, H, K, nsplit);
 }
@@ -1495,6 +1524,13 @@ int plan_cluster(int B, int max_n, int sms) {
     return nc;
 }
 
+smla_status check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return SMLA_OK;
+    if (bytes < need) return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
+    return aligned(workspace, 16) ? SMLA_OK : SMLA_ERR_MISALIGNED;
+}
+
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a != nullptr && b != nullptr && x < y + nb && y < x + na;
@@ -1541,9 +1577,10 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
     if (overlap(acc, cells, acc_new, cells) || overlap(pos, cells, pos_new, cells) ||
         overlap(n, (size_t)B * 4, n_new, (size_t)B * 4))
         return SMLA_ERR_INVALID_ARG;
-    if (workspace_bytes < smla_evict_workspace_bytes(B, max_n)) return SMLA_ERR_WORKSPACE_TOO_SMALL;
-    if (max_n > 0 && workspace == nullptr) return SMLA_ERR_INVALID_ARG;
-    if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
+    if (pos_new == nullptr) {
+        const smla_status st = check_workspace(workspace, workspace_bytes, smla_evict_workspace_bytes(B, max_n));
+        if (st != SMLA_OK) return st;
+    }
     smla::EvictPlanParams p{};
     p.acc = acc;
     p.pos = pos;
@@ -1553,7 +1590,7 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
     p.K = K;
     p.n_sink = n_sink;
     p.n_recent = n_recent;
-    p.movers = static_cast<int *>(workspace);
+    p.movers = pos_new == nullptr ? static_cast<int *>(workspace) : nullptr;
     p.src = src;
     p.n_new = n_new;
     p.acc_new = acc_new;
@@ -1603,11 +1640,19 @@ smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *pa
     p.pt_stride = pt_stride;
     p.num_pages = num_pages;
     p.n_buf = n_caches;
-    const long long units = (long long)B * ((K + smla::kApplySlots - 1ll) / smla::kApplySlots);
+    const long long units = (long long)B * ((K + 31ll) / 32);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (2 * 16 * p.total <= smla::kApplyBulkBytes) {
+        // two waves of the CTAs that fit: the second evens out what the first left
+        const long long most = 16ll * current_device_sms();
+        e = launch_dependent(smla::smla_evict_apply_bulk_kernel, (int)std::min(units, most), 32,
+                             smla::kApplyBulkBytes, st, p);
+        return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
+    }
     const long long blocks = (units + smla::kApplyWarps - 1) / smla::kApplyWarps;
     if (blocks > INT_MAX) return SMLA_ERR_INVALID_ARG;
-    const cudaError_t e = launch_dependent(smla::smla_evict_apply_kernel, (int)blocks, 32 * smla::kApplyWarps, 0,
-                                           static_cast<cudaStream_t>(stream), p);
+    e = launch_dependent(smla::smla_evict_apply_kernel, (int)blocks, 32 * smla::kApplyWarps, 0, st, p);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 

@@ -20,7 +20,7 @@ struct EvictPlanParams {
     const int *pos;      // [B, max_n] or null (slot i holds position i)
     const int *n;        // [B]
     int B, max_n, K, n_sink, n_recent;
-    int *movers;         // [B, max_n] scratch
+    int *movers;         // [B, max_n] scratch; null: what is behind slot m of pos_new serves until it is filled
     int *src;            // [B, K]
     int *n_new;          // [B]
     float *acc_new;      // [B, max_n] or null
@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
     int *src = p.src + (size_t)b * p.K;
     const int lo = (int)rank * p.per, hi = min(n, lo + p.per);  // this CTA's slots
     const bool cut = n > p.K;                                  // the same in the whole cluster
+    int *movers = p.movers != nullptr ? p.movers + base : p.pos_new + base + m;
     if (cut) {
         for (int i = tid; i < 3 * kPlanBins; i += kPlanThreads) hist[i] = 0u;
         // weights in, and the newest position
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
             const int mine = __popc(mvs);
             const int at_mv = ix_block_scan(mine, scratch, &total) - mine;
             int x = mv + at_mv;
-            for (uint32_t left = mvs; left; left &= left - 1u) p.movers[base + x++] = lo + 32 * w + __ffs(left) - 1;
+            for (uint32_t left = mvs; left; left &= left - 1u) movers[x++] = lo + 32 * w + __ffs(left) - 1;
             mv += total;
             const int gone = __popc(holes);
             const int at_hole = ix_block_scan(gone, scratch, &total) - gone;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
         }
         cluster_sync();  // the movers' list and pre are complete; no CTA leaves while another reads its counts
     }
-    // this CTA's slots, then its share of what lies behind n
+    // this CTA's slots below m, then its share of what lies behind
     auto put = [&](int i, int s) {
         if (i < p.K) src[i] = s;
         if (i < p.max_n) {
@@ -282,18 +283,19 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
         }
     };
 #pragma unroll 4
-    for (int i = lo + tid; i < hi; i += kPlanThreads) {
-        int s = i < m ? i : -1;
-        if (cut && i < m) {
+    for (int i = lo + tid; i < min(hi, m); i += kPlanThreads) {
+        int s = i;
+        if (cut) {
             const uint32_t k = keep[(i - lo) >> 5];
             if (!((k >> ((i - lo) & 31)) & 1u)) {
                 const uint32_t lower = (1u << ((i - lo) & 31)) - 1u;
-                s = ld_input(p.movers + base + pre[(i - lo) >> 5] + __popc(~k & lower));
+                s = ld_input(movers + pre[(i - lo) >> 5] + __popc(~k & lower));
             }
         }
         put(i, s);
     }
-    for (long long i = n + (long long)rank * kPlanThreads + tid; i < max(p.K, p.max_n); i += nc * kPlanThreads)
+    if (cut) cluster_sync();  // the movers have been read
+    for (long long i = m + (long long)rank * kPlanThreads + tid; i < max(p.K, p.max_n); i += nc * kPlanThreads)
         put((int)i, -1);
 }
 
@@ -313,35 +315,110 @@ struct EvictApplyParams {
     int n_buf;
     int total;                  // pieces of a row over all buffers
 };
+
+// One warp's share of the list entries [32 unit, 32 unit + 32) of the flattened
+// (sequence, entry) groups: where the row of this lane's entry comes from and
+// goes to, -1 where it stays.
+struct EvictMove {
+    long long from, to;  // rows of the pool: below 2^31
+};
+__device__ __forceinline__ int evict_entry(const EvictApplyParams &p, long long unit, long long per) {
+    const int i = (int)(unit % per) * 32 + (int)(threadIdx.x & 31);
+    return i < p.K ? ld_input(p.src + (size_t)(unit / per) * p.K + i) : -1;
+}
+__device__ __forceinline__ EvictMove evict_move(const EvictApplyParams &p, long long unit, long long per, int s) {
+    const int b = (int)(unit / per), i = (int)(unit % per) * 32 + (int)(threadIdx.x & 31);
+    EvictMove m{-1, -1};
+    if (s == -1 || s == i) return m;
+    const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
+    m.from = paged_row(pt_b, p.pt_stride, p.num_pages, s);
+    m.to = paged_row(pt_b, p.pt_stride, p.num_pages, i);
+    if (m.from < 0 || m.to < 0) {
+        count_bad_index();
+        m.from = m.to = -1;
+    }
+    return m;
+}
+
+// Rows that fit shared memory several times over (all real caches): one warp per
+// CTA, a lane per move.  Each lane has its row's pieces copied in by bulk copies
+// and, when the warp's have landed, out again: a few instructions per row, and
+// 28 KB per CTA, eight CTAs per SM, in flight.  (Moving 16-byte pieces through
+// registers took 65 instructions per 512 bytes, and 51 us where this takes 41,
+// 80000 rows of 1408 bytes: 5.5 TB/s.)
+constexpr int kApplyBulkBytes = 28160;  // twenty rows of 1152 + 256 bytes
+__global__ void __launch_bounds__(32) smla_evict_apply_bulk_kernel(const EvictApplyParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bar;
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long per = (p.K + 31) / 32, units = per * p.B;
+    const int row = 16 * p.total, most = kApplyBulkBytes / row;  // rows at a time
+    bool dead = false;
+    uint32_t phase = 0;
+    int s = evict_entry(p, blockIdx.x, per);
+    for (long long unit = blockIdx.x; unit < units && !dead; unit += gridDim.x) {
+        const EvictMove m = evict_move(p, unit, per, s);
+        if (unit + gridDim.x < units) s = evict_entry(p, unit + gridDim.x, per);
+        const uint32_t moves = __ballot_sync(0xffffffffu, m.from >= 0);
+        const int rank = __popc(moves & ((1u << lane) - 1u)), n = __popc(moves);
+        for (int k0 = 0; k0 < n; k0 += most) {
+            const bool mine = m.from >= 0 && rank >= k0 && rank < k0 + most;
+            uint8_t *at = smem + (rank - k0) * row;
+            if (lane == 0) mbar_arrive_expect_tx(&bar, (uint32_t)(min(most, n - k0) * row));
+            __syncwarp();
+            if (mine)
+                for (int k = 0, off = 0; k < p.n_buf; ++k) {
+                    const int bytes = 16 * p.pieces[k];
+                    bulk_g2s(at + off, p.buf[k] + m.from * bytes, (uint32_t)bytes, &bar);
+                    off += bytes;
+                }
+            mbar_wait(&bar, phase, dead);
+            phase ^= 1u;
+            if (mine && !dead) {
+                for (int k = 0, off = 0; k < p.n_buf; ++k) {
+                    const int bytes = 16 * p.pieces[k];
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                     __cvta_generic_to_global(p.buf[k] + m.to * bytes)),
+                                 "r"(smem_addr(at + off)), "r"(bytes)
+                                 : "memory");
+                    off += bytes;
+                }
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();  // the rows may be overwritten
+        }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 constexpr int kApplyWarps = 8;
 constexpr int kApplyDepth = 8;  // pieces in flight per lane
-constexpr int kApplySlots = 16; // list entries per warp
 
-// One warp per kApplySlots list entries.  It lists the moves among them, then its lanes
-// walk the moves' 16-byte pieces, all buffers in a row, eight loads in flight
-// each before the first store.  Bound by memory.
+// Longer rows.  One warp per 32 list entries: it lists the moves among them, then
+// its lanes walk the moves' 16-byte pieces, all buffers in a row, eight loads in
+// flight each before the first store.
 __global__ void __launch_bounds__(32 * kApplyWarps) smla_evict_apply_kernel(const EvictApplyParams p) {
-    __shared__ int from_s[kApplyWarps][kApplySlots], to_s[kApplyWarps][kApplySlots];
+    __shared__ int from_s[kApplyWarps][32], to_s[kApplyWarps][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long per = (p.K + kApplySlots - 1) / kApplySlots;
+    const long long per = (p.K + 31) / 32;
     const long long unit = (long long)blockIdx.x * kApplyWarps + warp;
     if (unit >= per * p.B) return;
-    const int b = (int)(unit / per), i = (int)(unit % per) * kApplySlots + lane;
-    const int s = lane < kApplySlots && i < p.K ? ld_input(p.src + (size_t)b * p.K + i) : -1;
-    long long from = -1, to = -1;  // rows of the pool: below 2^31
-    if (s != -1 && s != i) {
-        const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
-        from = paged_row(pt_b, p.pt_stride, p.num_pages, s);
-        to = paged_row(pt_b, p.pt_stride, p.num_pages, i);
-        if (from < 0 || to < 0) count_bad_index();
-    }
-    const uint32_t moves = __ballot_sync(0xffffffffu, from >= 0 && to >= 0);
+    const EvictMove m = evict_move(p, unit, per, evict_entry(p, unit, per));
+    const uint32_t moves = __ballot_sync(0xffffffffu, m.from >= 0);
     if ((moves >> lane) & 1u) {
         const int k = __popc(moves & ((1u << lane) - 1u));
-        from_s[warp][k] = (int)from;
-        to_s[warp][k] = (int)to;
+        from_s[warp][k] = (int)m.from;
+        to_s[warp][k] = (int)m.to;
     }
     __syncwarp();
     const int n = __popc(moves);

@@ -41,7 +41,7 @@ struct Q4Cfg {
     static constexpr int kThreads = 128;
     static constexpr int kRows = 16;                       // query rows (the mma's M)
     static constexpr int kTile = 64;                       // cache rows: one page
-    static constexpr int kStages = 2;
+    static constexpr int kStages = 3;
     static constexpr int kStageBytes = kTile * kQ4RowBytes;  // 26624
     static constexpr int kResolve = 512;                   // list entries resolved at a time
     static constexpr int kOffQ = 0;                        // uint4 [36][32]
@@ -49,7 +49,7 @@ struct Q4Cfg {
     static constexpr int kOffRows = kOffStage + kStages * kStageBytes;  // int [kResolve]
     static constexpr int kOffBar = kOffRows + kResolve * 4;
     static constexpr int kSmemBytes = kOffBar + 8 * kStages;
-    static constexpr int kMinBlocks = 3;                   // per SM: 3 x (73.8 + 1) KB
+    static constexpr int kMinBlocks = 2;                   // per SM: 2 x (100 + 1) KB
 };
 static_assert(Q4Cfg::kMinBlocks * (Q4Cfg::kSmemBytes + 1024) <= 233472, "shared memory per SM");
 
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
     // 26 16-byte pieces per row, 13 per thread and tile; padding slots are
     // zero-filled (scale 0: they decode to zeros)
     auto issue = [&](int it, int t, int n) {
-        const uint32_t dst = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
+        const uint32_t dst = sbase + C::kOffStage + it % C::kStages * C::kStageBytes;
 #pragma unroll
         for (int k = 0; k < 13; ++k) {
             const int e = tid + 128 * k, row = e / 26, ch = e - 26 * row;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
                          "r"(at >= 0 ? 16u : 0u)
                          : "memory");
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[it & 1]))
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[it % C::kStages]))
                      : "memory");
     };
 
@@ -397,16 +397,15 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
         resolve_rows<4>(p, bt, j0, base, n, rows_s, tid, C::kThreads);
         __syncthreads();
         const int tiles = (n + C::kTile - 1) / C::kTile;
-        issue(it, 0, n);
+        for (int t = 0; t < min(C::kStages, tiles); ++t) issue(it + t, t, n);
         if (!staged) {
             q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
             staged = true;
             __syncthreads();
         }
         for (int t = 0; t < tiles; ++t, ++it) {
-            const uint32_t tile = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
-            if (t + 1 < tiles && t == 0) issue(it + 1, 1, n);
-            mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
+            const uint32_t tile = sbase + C::kOffStage + it % C::kStages * C::kStageBytes;
+            mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1, dead);
             float sg[1][2][4];
             q4_scores<1>(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sg);
             float (&sc)[2][4] = sg[0];
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
             }
             w.softmax(tile, sc);
             __syncthreads();  // P complete; every warp is done with the previous tile
-            if (t >= 1 && t + 1 < tiles) issue(it + 1, t + 1, n);
+            if (t >= 1 && t - 1 + C::kStages < tiles) issue(it - 1 + C::kStages, t - 1 + C::kStages, n);
             w.output(tile);
         }
     }
@@ -504,11 +503,11 @@ __device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int n_units
                                              int *prefix, int *scratch) {
     const bool first_cta = blockIdx.x == 0;
     Q4Run r{};
+    int tiles = 0, incl = 0, sum = 0;
     for (int u0 = 0; u0 < n_units; u0 += blockDim.x) {
         const int u = u0 + threadIdx.x;
-        const int tiles = u < n_units ? (q4_unit_len(p, u, first_cta) + TILE - 1) / TILE : 0;
-        int sum;
-        const int incl = ix_block_scan(tiles, scratch, &sum);
+        tiles = u < n_units ? (q4_unit_len(p, u, first_cta) + TILE - 1) / TILE : 0;
+        incl = ix_block_scan(tiles, scratch, &sum);
         if (prefix != nullptr && first_cta && u < n_units) prefix[u] = (int)r.total + incl - tiles;
         r.total += sum;
     }
@@ -520,9 +519,10 @@ __device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int n_units
     long long before = 0;
     for (int u0 = 0; u0 < n_units && before <= r.begin; u0 += blockDim.x) {
         const int u = u0 + threadIdx.x;
-        const int tiles = u < n_units ? (q4_unit_len(p, u, false) + TILE - 1) / TILE : 0;
-        int sum;
-        const int incl = ix_block_scan(tiles, scratch, &sum);
+        if (n_units > (int)blockDim.x) {  // else the counts above are still those of this chunk
+            tiles = u < n_units ? (q4_unit_len(p, u, false) + TILE - 1) / TILE : 0;
+            incl = ix_block_scan(tiles, scratch, &sum);
+        }
         const long long first = before + incl - tiles;
         if (first <= r.begin && r.begin < first + tiles) {
             scratch[40] = u;
@@ -587,13 +587,12 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
         auto page_of = [&](int t) { return q4_page(pt_b, p.pt_stride, p.num_pages, t); };
         auto issue = [&](int i, int pg) {  // thread 0
-            q4_copy_page(p, pg, smem + C::kOffStage + (i & 1) * C::kStageBytes, &full[i & 1]);
+            q4_copy_page(p, pg, smem + C::kOffStage + i % C::kStages * C::kStageBytes, &full[i % C::kStages]);
         };
         fence_proxy_async_smem();
         __syncthreads();  // the previous piece is done with the ring and with Q
         if (tid == 0) {
-            issue(it, page_of(tile0));
-            if (tiles > 1) issue(it + 1, page_of(tile0 + 1));
+            for (int t = 0; t < min(C::kStages, tiles); ++t) issue(it + t, page_of(tile0 + t));
         }
         q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, row0, nrows);
         // visible positions of this lane's two query rows
@@ -605,12 +604,12 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         w.reset();
         __syncthreads();
         for (int t = 0; t < tiles; ++t, ++it) {
-            const uint32_t tile = sbase + C::kOffStage + (it & 1) * C::kStageBytes;
+            const uint32_t tile = sbase + C::kOffStage + it % C::kStages * C::kStageBytes;
             const int pos0 = (tile0 + t) * C::kTile;
             const bool mapped = page_of(tile0 + t) >= 0;
             int next = -1;
-            if (tid == 0 && t >= 1 && t + 1 < tiles) next = page_of(tile0 + t + 1);
-            mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
+            if (tid == 0 && t >= 1 && t - 1 + C::kStages < tiles) next = page_of(tile0 + t - 1 + C::kStages);
+            mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1, dead);
             // rows that no query token sees may hold anything: scale 0 makes
             // them decode to zeros (0 * P = 0)
             const int live = mapped ? min(len - pos0, C::kTile) : 0;
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
             w.softmax(tile, sc);
             fence_proxy_async_smem();  // P and cleared scales, before a later bulk copy writes there
             __syncthreads();  // P complete; every warp is done with the previous tile
-            if (tid == 0 && t >= 1 && t + 1 < tiles) issue(it + 1, next);
+            if (tid == 0 && t >= 1 && t - 1 + C::kStages < tiles) issue(it - 1 + C::kStages, next);
             w.output(tile);
         }
         // ---- the piece

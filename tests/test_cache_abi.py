@@ -83,8 +83,8 @@ REFUSALS = [
     (plan, dict(B=-1), INVALID), (plan, dict(K=0), INVALID), (plan, dict(sink=-1), INVALID),
     (plan, dict(sink=40, recent=11), INVALID), (plan, dict(sink=2**31 - 1, recent=2**31 - 1), INVALID),
     (plan, dict(max_n=524289), UNSUPPORTED), (plan, dict(n=None), INVALID), (plan, dict(src=None), INVALID),
-    (plan, dict(acc=None), INVALID), (plan, dict(n_new=None), INVALID), (plan, dict(wsb=799), SMALL),
-    (plan, dict(ws=None), INVALID), (plan, dict(ws=FAKE + 4), MISALIGNED), (plan, dict(acc_new=FAKE), INVALID),
+    (plan, dict(acc=None), INVALID), (plan, dict(n_new=None), INVALID), (plan, dict(wsb=799, pos_new=None), SMALL),
+    (plan, dict(ws=None, pos_new=None), INVALID), (plan, dict(ws=FAKE + 4, pos_new=None), MISALIGNED), (plan, dict(acc_new=FAKE), INVALID),
     (plan, dict(acc_new=FAKE + 796), INVALID), (plan, dict(pos_new=FAKE), INVALID), (plan, dict(n_new=FAKE + 4), INVALID),
     (plan, dict(pos=FAKE + 2), MISALIGNED),
     (apply, dict(B=-1), INVALID), (apply, dict(src=None), INVALID), (apply, dict(src=FAKE + 1), MISALIGNED),
@@ -119,7 +119,13 @@ def test_workspace_sizes_and_splits(lib):
     assert binding.dense_q4_workspace_bytes(2, 3, 8, 4096, 5) == binding.workspace_bytes(2, 3, 8, 5)
     for S in (1, 7):  # up to 16 query rows: pieces of (splits + 1) per unit, their maxima, the tiles before each unit
         assert binding.dense_q4_workspace_bytes(3, 2, 8, 4096, S) == r(3 * (S + 1) * 16 * 2048) + r(3 * (S + 1) * 16 * 8) + r(16)
-    assert binding.dense_q4_workspace_bytes(2, 1, 16, 4096, 0) == 0
+    assert binding.q4_workspace_bytes(2, 1, 16, 2048, 1) == 0
+    assert binding.q4_workspace_bytes(2, 3, 8, 2048, 5) == binding.workspace_bytes(2, 3, 8, 5)
+    for B, T, H in [(1, 1, 16), (3, 5, 8), (60, 1, 64)]:  # 0: the default's
+        assert binding.q4_workspace_bytes(B, T, H, 2048) == binding.q4_workspace_bytes(B, T, H, 2048, binding.q4_nsplit(B, T, H, 2048))
+        assert binding.dense_q4_workspace_bytes(B, T, H, 9000) == binding.dense_q4_workspace_bytes(
+            B, T, H, 9000, binding.dense_q4_nsplit(B, T, H, 9000))
+    assert [binding.q4_nsplit(b, 1, 16, 2048) for b in (1, 15, 64, 1000)] == [32, 16, 4, 1]  # on 148 SMs
     for B, T, H, K in [(1, 1, 16, 2048), (64, 1, 16, 2048), (60, 1, 64, 2048), (3, 5, 8, 1999)]:
         assert 1 <= binding.q4_nsplit(B, T, H, K) <= 1024
         assert 1 <= binding.dense_q4_nsplit(B, T, H, 20 * K) <= 1024

@@ -186,6 +186,18 @@ def test_plan_keeps_sinks_and_recent_positions(n_sink, n_recent):
     run_plan(acc, [400, 399, 130], 100, n_sink=n_sink, n_recent=n_recent)
 
 
+def test_plan_without_positions_out():
+    """The C entry point without acc_new and pos_new: the list of movers goes to the workspace."""
+    acc = torch.rand(3, 900, generator=torch.Generator().manual_seed(1)).cuda()
+    n = torch.tensor([900, 500, 20], dtype=torch.int32).cuda()
+    want = binding.evict_plan(acc, n, 300)
+    src, m = torch.empty_like(want.src), torch.empty_like(n)
+    ws = torch.empty(binding.evict_workspace_bytes(3, 900), dtype=torch.uint8, device="cuda")
+    st = binding.lib().smla_evict_plan(acc.data_ptr(), None, n.data_ptr(), 3, 900, 300, 0, 0, ws.data_ptr(), ws.numel(),
+                                       src.data_ptr(), m.data_ptr(), None, None, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(src, want.src) and torch.equal(m, want.n)
+
+
 def test_plan_far_positions():
     acc = np.arange(40, dtype=np.float64)[None]
     pos = (np.arange(40)[None] + 2 ** 31 - 40).astype(np.int32)
@@ -219,6 +231,19 @@ def test_apply_moves_rows_of_every_buffer(n, K):
                 for i in range(min(n[b], K)):
                     want[paged.row(b, i)] = old[paged.row(b, src[b, i])]
             np.testing.assert_array_equal(buf.view(torch.uint8).cpu().numpy().reshape(paged.pages * 64, -1), want)
+
+
+def test_apply_long_rows():
+    """Rows of 20 KB: longer than the bulk form takes."""
+    paged = cu.Paged([150], 3)
+    buf = torch.randint(0, 256, (paged.pages, 64, 20480), dtype=torch.uint8, generator=torch.Generator().manual_seed(1)).cuda()
+    old = buf.clone().view(-1, 20480)
+    p = binding.evict_plan(torch.rand(1, 150, generator=torch.Generator().manual_seed(2)).cuda(), torch.tensor([150], dtype=torch.int32).cuda(), 70)
+    binding.evict_apply(p.src, paged.cuda, (buf,))
+    want = old.clone()
+    to = torch.from_numpy(paged.rows(0, range(70))).cuda()
+    want[to] = old[torch.from_numpy(paged.rows(0, p.src[0].tolist())).cuda()]
+    assert torch.equal(buf.view(-1, 20480), want)
 
 
 def test_apply_leaves_out_and_counts_unmapped_rows():
