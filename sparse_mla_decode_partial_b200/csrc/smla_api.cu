@@ -1300,7 +1300,8 @@ smla_status smla_q4_read(const void *cache_q4, int64_t num_pages, const int32_t 
 
 int smla_q4_nsplit(int B, int T, int H, int K) {
     if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
-    if (H > kQ4Rows) return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
+    // (SMLA_NSPLIT overrides every heuristic alike)
+    if (H > kQ4Rows || std::getenv("SMLA_NSPLIT")) return smla_choose_nsplit(B, T, smla::kMaxTcRows, K, 0);
     return q4_sparse_nsplit((long long)B * T, K, current_device_sms());
 }
 
@@ -1343,7 +1344,7 @@ smla_status smla_decode_q4(const void *q, const void *cache_q4, int64_t num_page
 
 int smla_dense_q4_nsplit(int B, int T, int H, int K) {
     if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
-    if (!q4_dense_small(T, H)) return smla_dense_nsplit(B, T, H, K);
+    if (!q4_dense_small(T, H) || std::getenv("SMLA_NSPLIT")) return smla_dense_nsplit(B, T, H, K);
     // one full wave of CTAs
     const long long n = (long long)B * q4_dense(B, T, H, 1).units;
     const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();

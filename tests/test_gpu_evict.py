@@ -258,6 +258,46 @@ def test_apply_leaves_out_and_counts_unmapped_rows():
     np.testing.assert_array_equal(buf.cpu().numpy().reshape(-1, 32), want)
 
 
+def test_plan_of_empty_sequences():
+    p = binding.evict_plan(torch.empty(2, 0).cuda(), torch.zeros(2, dtype=torch.int32).cuda(), 5)
+    assert p.src.tolist() == [[-1] * 5] * 2 and p.n.tolist() == [0, 0] and p.acc.shape == (2, 0)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_accumulate_plan_apply_in_a_graph_and_on_another_stream(q4):
+    paged = cu.Paged([500, 300], 1)
+    start, _ = make_cache(paged, q4, 2)
+    table, q = paged.cuda, cu.queries(2, 1, 16, 3).cuda()
+    n = torch.tensor([500, 300], dtype=torch.int32).cuda()
+    lens, lse = n[:, None].contiguous(), torch.full((2, 1, 16), 6.0).cuda()
+
+    def steps(cache, acc, stream=None):
+        binding.evict_accumulate(q, cache, table, lens, lse, SCALE, acc, stream=stream)
+        p = binding.evict_plan(acc, n, 256, n_sink=4, n_recent=32, stream=stream)
+        binding.evict_apply(p.src, table, (cache,), stream=stream)
+        return p
+
+    want_cache, want_acc = start.clone(), torch.zeros(2, 500).cuda()
+    want = steps(want_cache, want_acc)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    cache, acc = start.clone(), torch.zeros(2, 500).cuda()
+    side.wait_stream(torch.cuda.current_stream())
+    got = steps(cache, acc, stream=side)
+    side.synchronize()
+    assert torch.equal(cache.view(torch.uint8), want_cache.view(torch.uint8)) and all(torch.equal(a, b) for a, b in zip(got, want))
+    cache, acc = start.clone(), torch.zeros(2, 500).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = steps(cache, acc)
+    for _ in range(2):
+        cache.copy_(start)
+        acc.zero_()
+        graph.replay()
+        assert torch.equal(acc, want_acc) and torch.equal(cache.view(torch.uint8), want_cache.view(torch.uint8))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("q4", [False, True])
 def test_a_cache_lives_through_steps_and_evictions(q4):

@@ -206,13 +206,13 @@ def run_sparse(lens, T, H, idx, nsplit, seed=0, what="", **kw):
 
 
 @pytest.mark.parametrize("H", [1, 3, 8, 15, 16, 17, 32, 33, 64])
-@pytest.mark.parametrize("nsplit", [0, 1, 3])
+@pytest.mark.parametrize("nsplit", [0, 1, 2, 3, 16])
 def test_sparse_heads(H, nsplit):
     run_sparse([300, 90], 2, H, lists_for([300, 90], 2, 130, H, hole=0.1), nsplit, seed=H)
 
 
 @pytest.mark.parametrize("K", [0, 1, 7, 31, 32, 33, 63, 64, 65, 127, 200, 513])
-@pytest.mark.parametrize("H,nsplit", [(16, 0), (16, 1), (16, 4), (64, 2), (5, 70)])
+@pytest.mark.parametrize("H,nsplit", [(16, 0), (16, 1), (16, 4), (16, 5), (7, 8), (64, 2), (5, 70)])
 def test_sparse_widths(K, H, nsplit):
     run_sparse([600], 1, H, lists_for([600], 1, K, K), nsplit, seed=K + 1)
 
@@ -297,6 +297,88 @@ def test_sparse_on_another_stream_in_two_graphs_and_twice_the_same():
         out[0].zero_()
         g.replay()
         assert torch.equal(o, out[0]) and torch.equal(lse, out[1])
+
+
+def test_calls_from_two_threads_on_two_streams():
+    """Two host threads decode at once, each on a stream of its own, over one cache."""
+    import threading
+    lens = [900, 800]
+    paged = cu.Paged(lens, 2)
+    cache, vals = fill(paged, lens, 3)
+    table = paged.cuda
+    idx = torch.from_numpy(lists_for(lens, 1, 500, 1)).cuda()
+    seq = torch.tensor([[900], [800]], dtype=torch.int32).cuda()
+    qs = [cu.queries(2, 1, 16, 4 + k).cuda() for k in range(2)]
+    want = [(binding.decode_q4(q, cache, table, idx, SCALE), binding.decode_dense_q4(q, cache, table, seq, SCALE, K=900)) for q in qs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = (binding.decode_q4(qs[k], cache, table, idx, SCALE), binding.decode_dense_q4(qs[k], cache, table, seq, SCALE, K=900))
+                stream.synchronize()
+                bad.extend(not torch.equal(x, y) for a, b in zip(got, want[k]) for x, y in zip(a, b))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(bad) == 2 * 20 * 4 and not any(bad)
+
+
+@pytest.mark.parametrize("T,H", [(1, 16), (2, 40)])
+def test_dense_in_two_graphs(T, H):
+    lens = [[700 - t for t in range(T)][::-1], [130 - t for t in range(T)][::-1]]
+    paged = cu.Paged([700, 130], 2)
+    cache, vals = fill(paged, lens, 3)
+    table, q = paged.cuda, cu.queries(2, T, H, 4).cuda()
+    seq = torch.tensor(lens, dtype=torch.int32).cuda()
+    o, lse = binding.decode_dense_q4(q, cache, table, seq, SCALE, K=700)
+    graphs = []
+    for _ in range(2):
+        g, out = torch.cuda.CUDAGraph(), (torch.empty_like(o), torch.empty_like(lse))
+        with torch.cuda.graph(g):
+            binding.decode_dense_q4(q, cache, table, seq, SCALE, K=700, o=out[0], lse=out[1])
+        graphs.append((g, out))
+    for g, out in graphs + graphs:
+        out[0].zero_()
+        g.replay()
+        assert torch.equal(o, out[0]) and torch.equal(lse, out[1])
+
+
+def test_binding_refuses_what_the_kernels_cannot_read():
+    paged = cu.Paged([64])
+    cache, _ = fill(paged, None, 1)
+    q, table = cu.queries(1, 1, 8, 1).cuda(), paged.cuda
+    idx, lens = torch.zeros(1, 1, 4, dtype=torch.int32).cuda(), torch.ones(1, 1, dtype=torch.int32).cuda()
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache[:, :, :400].contiguous(), table, idx, SCALE)
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache.transpose(0, 1), table, idx, SCALE)
+    with pytest.raises(TypeError):
+        binding.decode_q4(q, cache, table, idx.long(), SCALE)
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache, table, idx[:, 0], SCALE)
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache, torch.cat([table, table]), idx, SCALE)
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache, table, idx.cpu(), SCALE)
+    with pytest.raises(ValueError):
+        binding.decode_q4(q, cache, table, idx, SCALE, o=torch.empty(1, 1, 8, 511, dtype=torch.bfloat16).cuda())
+    with pytest.raises(binding.SmlaError):
+        binding.decode_q4(q, cache, table, torch.zeros(1, 1, 400, dtype=torch.int32).cuda(), SCALE, 3, workspace=torch.empty(64, dtype=torch.uint8).cuda())
+    with pytest.raises(binding.SmlaError):
+        binding.decode_dense_q4(q, cache, table, lens, float("inf"))
+    with pytest.raises(binding.SmlaError):
+        shifted = torch.empty(8 * 576 + 1, dtype=torch.bfloat16).cuda()[1:].view(1, 1, 8, 576)
+        binding.decode_dense_q4(shifted, cache, table, lens, SCALE)
+    with pytest.raises(ValueError):
+        binding.q4_append(q.view(8, 576), cache, table, torch.zeros(1, dtype=torch.int32).cuda(), lens[0])
+    with pytest.raises(ValueError):
+        binding.q4_read(cache, table, idx)
 
 
 # ---------------------------------------------------------------- dense decode
