@@ -538,7 +538,7 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  * 2. smla_evict_plan chooses, for each sequence of n[b] slots, the
  *    m = min(n[b], K) that stay, and which row each slot gets:
  *      pos  int32 [B, max_n], or NULL: the original position of the token in
- *           slot i (NULL: i).  Tokens with pos < n_sink, and those with
+ *           slot i (NULL: i), distinct within a sequence.  Tokens with pos < n_sink, and those with
  *           pos >= (largest pos) + 1 - n_recent, stay whatever their weight;
  *           n_sink + n_recent <= K.
  *      The others rank by acc, larger first; NaN counts as -inf; equal weights
@@ -552,8 +552,8 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  *      n_new int32 [B]: m.
  *      acc_new fp32, pos_new int32 [B, max_n], either may be NULL: acc and pos
  *           carried along (slot i from src[b, i]); 0 and -1 from m on.
- *    acc_new, pos_new and n_new must not overlap acc, pos and n
- *    (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
+ *    src, n_new, acc_new and pos_new must overlap neither one another nor acc,
+ *    pos and n (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
  *    outside [0, max_n] is clamped and counted.  workspace is used only where
  *    pos_new is NULL (it may be NULL otherwise): device, 16-B aligned, at least
  *    smla_evict_workspace_bytes(B, max_n).
@@ -567,7 +567,9 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  *                (1152 for the bf16 latent cache, 416 for the 4-bit one, 256
  *                for the index keys)
  *    With a src that smla_evict_plan wrote the moves are independent, and
- *    applying them twice changes nothing.  An entry whose source or destination
+ *    applying them twice changes nothing; with any other list where one entry's
+ *    source is another's destination, which row such a copy reads is undefined.
+ *    An entry whose source or destination
  *    no page maps is left out and counted.  Pages must not be shared with
  *    another sequence.
  */

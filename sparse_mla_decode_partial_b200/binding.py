@@ -639,10 +639,11 @@ def decode_q4(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, works
     b, t, K = _dims(idx, 3, "idx must be [B,T,K]")
     if b != B or t != T:
         raise ValueError("idx must be [B,T,K]")
+    nsplit = int(nsplit)
     need = q4_workspace_bytes(B, T, H, K, nsplit) if workspace is None else 0
     workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
     _launch("smla_decode_q4", dev, stream, q.data_ptr(), cache.data_ptr(), num_pages, page_table.data_ptr(),
-            pt_stride, idx.data_ptr(), B, T, H, _k_in_range(K), PAGE_SIZE, scale, nsplit,
+            pt_stride, idx.data_ptr(), B, T, H, _k_in_range(K), PAGE_SIZE, float(scale), nsplit,
             workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
     return o, lse
 
@@ -658,10 +659,11 @@ def decode_dense_q4(q, cache, page_table, seq_lens, scale: float, nsplit: int = 
     if K is None:
         K = int(seq_lens.max().item()) if seq_lens.numel() else 0
     K = _k_in_range(int(K))
+    nsplit = int(nsplit)
     need = dense_q4_workspace_bytes(B, T, H, K, nsplit) if workspace is None else 0
     workspace, o, lse = _decode_out(dev, B, T, H, need, workspace, o, lse, stream)
     _launch("smla_decode_dense_q4", dev, stream, q.data_ptr(), cache.data_ptr(), num_pages,
-            page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), B, T, H, K, PAGE_SIZE, scale, nsplit,
+            page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), B, T, H, K, PAGE_SIZE, float(scale), nsplit,
             workspace.data_ptr(), workspace.numel(), o.data_ptr(), lse.data_ptr())
     return o, lse
 
@@ -701,7 +703,7 @@ def evict_accumulate(q, cache, page_table, seq_lens, lse, scale: float, acc, *, 
         raise ValueError("acc must be [B, max_n]")
     _launch("smla_evict_accumulate_q4" if q4 else "smla_evict_accumulate", dev, stream, q.data_ptr(),
             cache.data_ptr(), num_pages, page_table.data_ptr(), pt_stride, seq_lens.data_ptr(), lse.data_ptr(),
-            B, T, H, PAGE_SIZE, scale, acc.data_ptr(), _k_in_range(max_n))
+            B, T, H, PAGE_SIZE, float(scale), acc.data_ptr(), _k_in_range(max_n))
     return acc
 
 
@@ -715,7 +717,7 @@ def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, 
     _need(acc, torch.float32, "acc")
     dev = acc.device
     B, max_n = _dims(acc, 2, "acc must be [B, max_n]")
-    K = _k_in_range(int(K))
+    K, n_sink, n_recent = _k_in_range(int(K)), _k_in_range(int(n_sink)), _k_in_range(int(n_recent))
     if K < 1:
         raise ValueError("K must be at least 1")
     _want(n, torch.int32, "n", dev, (B,))

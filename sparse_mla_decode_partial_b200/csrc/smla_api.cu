@@ -1217,27 +1217,22 @@ int q4_sparse_nsplit(long long bt, int K, int sms) {
     return best;
 }
 
-// The dense schedule over packed units of at most kQ4Rows query rows.
+// The dense schedule of sequences with at most kQ4Rows query rows in all.
 constexpr int kQ4MinTiles = 2;
 bool q4_dense_small(int T, int H) { return (long long)T * H <= kQ4Rows; }
 struct Q4Dense {
-    int pack, units;         // tokens per unit, units per sequence
-    long long n_units, ctas;
+    long long ctas;
     size_t off_ml, off_prefix, bytes;
 };
-Q4Dense q4_dense(int B, int T, int H, int nsplit) {
+Q4Dense q4_dense(int B, int nsplit) {
     Q4Dense d{};
-    const int most = std::max(1, std::min(T, kQ4Rows / std::max(H, 1)));
-    d.units = (T + most - 1) / most;
-    d.pack = (T + d.units - 1) / d.units;
-    d.n_units = (long long)B * d.units;
-    // nsplit CTAs per unit, but no more than run at once
+    // nsplit CTAs per sequence, but no more than run at once
     const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();
-    d.ctas = std::min(d.n_units * nsplit, std::max(slots, d.n_units));
-    const size_t rows = (size_t)(d.ctas + d.n_units) * kQ4Rows;
+    d.ctas = std::min((long long)B * nsplit, std::max<long long>(slots, B));
+    const size_t rows = (size_t)(d.ctas + B) * kQ4Rows;
     d.off_ml = round256(rows * smla::kDc * sizeof(float));
     d.off_prefix = d.off_ml + round256(rows * sizeof(float2));
-    d.bytes = d.off_prefix + round256((size_t)(d.n_units + 1) * sizeof(int));
+    d.bytes = d.off_prefix + round256(((size_t)B + 1) * sizeof(int));
     return d;
 }
 
@@ -1346,15 +1341,14 @@ int smla_dense_q4_nsplit(int B, int T, int H, int K) {
     if (B <= 0 || T <= 0 || H <= 0 || H > SMLA_MAX_HEADS || K <= 0) return 1;
     if (!q4_dense_small(T, H) || std::getenv("SMLA_NSPLIT")) return smla_dense_nsplit(B, T, H, K);
     // one full wave of CTAs
-    const long long n = (long long)B * q4_dense(B, T, H, 1).units;
     const long long slots = (long long)smla::Q4Cfg::kMinBlocks * current_device_sms();
-    return (int)std::max<long long>(1, std::min<long long>(SMLA_MAX_NSPLIT, (slots + n - 1) / n));
+    return (int)std::min<long long>(SMLA_MAX_NSPLIT, (slots + B - 1) / B);
 }
 
 size_t smla_dense_q4_workspace_bytes(int B, int T, int H, int K, int nsplit) {
     if (B < 0 || T < 0 || H < 0 || K < 0 || nsplit < 0 || nsplit > SMLA_MAX_NSPLIT) return 0;
     if (nsplit == 0) nsplit = smla_dense_q4_nsplit(B, T, H, K);
-    if (q4_dense_small(T, H)) return q4_dense(B, T, H, nsplit).bytes;
+    if (q4_dense_small(T, H)) return q4_dense(B, nsplit).bytes;
     return smla_dense_workspace_bytes(B, T, H, K, nsplit);
 }
 
@@ -1373,25 +1367,21 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (q4_dense_small(T, H)) {
         if (nsplit == 0) nsplit = smla_dense_q4_nsplit(B, T, H, K);
-        const Q4Dense d = q4_dense(B, T, H, nsplit);
-        if (d.ctas + d.n_units > INT_MAX / kQ4Rows || d.n_units * ((K + 63ll) / 64) > INT_MAX)
+        const Q4Dense d = q4_dense(B, nsplit);
+        if (d.ctas + B > INT_MAX / kQ4Rows || B * ((K + 63ll) / 64) > INT_MAX)
             return SMLA_ERR_INVALID_ARG;
         if (workspace_bytes < d.bytes) return SMLA_ERR_WORKSPACE_TOO_SMALL;
         if (workspace == nullptr) return SMLA_ERR_INVALID_ARG;
         if (!aligned(workspace, 16)) return SMLA_ERR_MISALIGNED;
         smla::Q4Params a{};
-        a.p = make_params(q, cache_q4, num_pages, page_table, pt_stride, nullptr, B, d.units, d.pack * H, K,
-                          scale, 1);
+        a.p = make_params(q, cache_q4, num_pages, page_table, pt_stride, nullptr, B, 1, T * H, K, scale, 1);
         a.p.seq_lens = seq_lens;
-        a.p.pack = d.pack;
         a.p.dense_t = T;
         a.p.dense_h = H;
         a.p.o = static_cast<__nv_bfloat16 *>(o);
         a.p.lse = lse;
-        a.dense = 1;
         a.grid = (int)d.ctas;
         a.min_tiles = kQ4MinTiles;
-        a.n_units = (int)d.n_units;
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         a.piece_o = reinterpret_cast<float *>(ws);
         a.piece_ml = reinterpret_cast<float2 *>(ws + d.off_ml);
@@ -1506,7 +1496,7 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
     smla::WeighParams a{};
     a.p = make_params(q, cache, num_pages, page_table, pt_stride, nullptr, B, 1, (int)rows, max_n, scale, 1);
     a.p.seq_lens = seq_lens;
-    a.p.pack = a.p.dense_t = T;
+    a.p.dense_t = T;
     a.p.dense_h = H;
     a.lse = lse;
     a.acc = acc;
@@ -1534,7 +1524,7 @@ smla_status check_workspace(const void *workspace, size_t bytes, size_t need) {
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+    return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
 }  // namespace
@@ -1575,9 +1565,14 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
         !aligned(acc_new, 4) || !aligned(pos_new, 4))
         return SMLA_ERR_MISALIGNED;
     const size_t cells = (size_t)B * max_n * 4;
-    if (overlap(acc, cells, acc_new, cells) || overlap(pos, cells, pos_new, cells) ||
-        overlap(n, (size_t)B * 4, n_new, (size_t)B * 4))
-        return SMLA_ERR_INVALID_ARG;
+    const struct {
+        const void *at;
+        size_t bytes;
+    } buf[] = {{src, (size_t)B * K * 4}, {n_new, (size_t)B * 4}, {acc_new, cells}, {pos_new, cells},  // outputs
+               {acc, cells}, {pos, cells}, {n, (size_t)B * 4}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (overlap(buf[i].at, buf[i].bytes, buf[j].at, buf[j].bytes)) return SMLA_ERR_INVALID_ARG;
     if (pos_new == nullptr) {
         const smla_status st = check_workspace(workspace, workspace_bytes, smla_evict_workspace_bytes(B, max_n));
         if (st != SMLA_OK) return st;

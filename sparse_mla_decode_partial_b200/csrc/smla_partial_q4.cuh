@@ -1,6 +1,6 @@
 // smla_partial_q4.cuh -- split-K partial pass over 4-bit cache rows for up to
-// 16 query rows (heads of one token, or of several tokens that share a dense
-// prefix), and the combine of the dense schedule's pieces.
+// 16 query rows (heads of one token, or of all tokens of a sequence that share
+// a dense prefix), and the combine of the dense schedule's pieces.
 //
 // At 416 bytes a row the memory can deliver one row per SM about every 18
 // cycles, so what counts is the work per row: decoding 512 codes, 2 * 16 * 1088
@@ -53,19 +53,17 @@ struct Q4Cfg {
 };
 static_assert(Q4Cfg::kMinBlocks * (Q4Cfg::kSmemBytes + 1024) <= 233472, "shared memory per SM");
 
-// The dense schedule: units (packed query tokens of one sequence) have
-// ceil(longest visible length / 64) tiles; CTA c of `grid` takes an equal run
-// of the flattened tiles and writes one piece per unit it meets, piece (c, u)
-// at slot c + u (c + u grows strictly along the run, so slots are distinct).
+// The dense schedule: sequence b has ceil(its longest visible length / 64)
+// tiles; CTA c of `grid` takes an equal run of the flattened tiles and writes
+// one piece per sequence it meets, piece (c, b) at slot c + b (c + b grows
+// strictly along the run, so slots are distinct).
 struct Q4Params {
-    PartialParams p;
-    int dense;
-    int grid;          // dense: CTAs that share the tiles
-    int min_tiles;     // dense: fewest tiles worth a CTA
-    int *prefix;       // dense: [n_units + 1] tiles before each unit, written by CTA 0
-    int n_units;
-    float *piece_o;    // [grid + n_units, 16, 512]
-    float2 *piece_ml;  // [grid + n_units, 16]: (max, lse) in log2 units
+    PartialParams p;   // dense_t tokens of dense_h heads, at most 16 rows together
+    int grid;          // CTAs that share the tiles
+    int min_tiles;     // fewest tiles worth a CTA
+    int *prefix;       // [B + 1] tiles before each sequence, written by CTA 0
+    float *piece_o;    // [grid + B, 16, 512]
+    float2 *piece_ml;  // [grid + B, 16]: (max, lse) in log2 units
 };
 
 // Cache row (0..7 of its n8 tile) that column n of a B fragment stands for.
@@ -472,12 +470,11 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
 }
 
 // ---------------------------------------------------------------- dense prefixes
-// Longest visible length of unit u's query tokens; lengths outside [0, K] are
-// clamped (and counted when `count`).
-__device__ __forceinline__ int q4_unit_len(const PartialParams &p, int u, bool count) {
-    const int b = u / p.T, t0 = (u - b * p.T) * p.pack, t1 = min(t0 + p.pack, p.dense_t);
+// Longest visible length of sequence b's query tokens; lengths outside [0, K]
+// are clamped (and counted when `count`).
+__device__ __forceinline__ int q4_seq_len(const PartialParams &p, int b, bool count) {
     int len = 0;
-    for (int t = t0; t < t1; ++t) {
+    for (int t = 0; t < p.dense_t; ++t) {
         const int raw = ld_input(p.seq_lens + (size_t)b * p.dense_t + t);
         if (count && (raw < 0 || raw > p.K)) count_bad_index();
         len = max(len, min(max(raw, 0), p.K));
@@ -492,46 +489,46 @@ __host__ __device__ __forceinline__ int q4_sharers(int grid, int min_tiles, long
 }
 
 // A CTA's run [begin, end) of the flattened tiles of TILE positions: total
-// first, then the unit and the tile it starts in.  Every thread calls it;
-// scratch holds 48 ints of shared memory.  count: report bad lengths (one CTA).
+// first, then the sequence and the tile it starts in.  Every thread calls it;
+// scratch holds 48 ints of shared memory.  The first CTA counts bad lengths.
 struct Q4Run {
     long long total, begin, end;
-    int unit, tile;
+    int b, tile;
 };
 template <int TILE>
-__device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int n_units, int grid, int min_tiles,
-                                             int *prefix, int *scratch) {
+__device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int grid, int min_tiles, int *prefix,
+                                             int *scratch) {
     const bool first_cta = blockIdx.x == 0;
     Q4Run r{};
     int tiles = 0, incl = 0, sum = 0;
-    for (int u0 = 0; u0 < n_units; u0 += blockDim.x) {
-        const int u = u0 + threadIdx.x;
-        tiles = u < n_units ? (q4_unit_len(p, u, first_cta) + TILE - 1) / TILE : 0;
+    for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        tiles = b < p.B ? (q4_seq_len(p, b, first_cta) + TILE - 1) / TILE : 0;
         incl = ix_block_scan(tiles, scratch, &sum);
-        if (prefix != nullptr && first_cta && u < n_units) prefix[u] = (int)r.total + incl - tiles;
+        if (prefix != nullptr && first_cta && b < p.B) prefix[b] = (int)r.total + incl - tiles;
         r.total += sum;
     }
-    if (prefix != nullptr && first_cta && threadIdx.x == 0) prefix[n_units] = (int)r.total;
+    if (prefix != nullptr && first_cta && threadIdx.x == 0) prefix[p.B] = (int)r.total;
     const int sharers = q4_sharers(grid, min_tiles, r.total);
     if ((int)blockIdx.x >= sharers || r.total == 0) return r;
     r.begin = r.total * blockIdx.x / sharers;
     r.end = r.total * (blockIdx.x + 1) / sharers;
     long long before = 0;
-    for (int u0 = 0; u0 < n_units && before <= r.begin; u0 += blockDim.x) {
-        const int u = u0 + threadIdx.x;
-        if (n_units > (int)blockDim.x) {  // else the counts above are still those of this chunk
-            tiles = u < n_units ? (q4_unit_len(p, u, false) + TILE - 1) / TILE : 0;
+    for (int b0 = 0; b0 < p.B && before <= r.begin; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        if (p.B > (int)blockDim.x) {  // else the counts above are still those of this chunk
+            tiles = b < p.B ? (q4_seq_len(p, b, false) + TILE - 1) / TILE : 0;
             incl = ix_block_scan(tiles, scratch, &sum);
         }
         const long long first = before + incl - tiles;
         if (first <= r.begin && r.begin < first + tiles) {
-            scratch[40] = u;
+            scratch[40] = b;
             scratch[41] = (int)(r.begin - first);
         }
         before += sum;
     }
     __syncthreads();
-    r.unit = scratch[40];
+    r.b = scratch[40];
     r.tile = scratch[41];
     return r;
 }
@@ -571,19 +568,17 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const Q4Run run = q4_find_run<C::kTile>(p, a.n_units, a.grid, a.min_tiles, a.prefix, scratch);
-    int unit = run.unit, tile0 = run.tile;
+    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, a.min_tiles, a.prefix, scratch);
+    const int nrows = p.dense_t * p.dense_h;
+    int b = run.b, tile0 = run.tile;
     Q4Consumer w;
     w.init(warp, lane);
     int it = 0;
-    for (long long at = run.begin; at < run.end; ++unit, tile0 = 0) {
-        const int len = q4_unit_len(p, unit, false);
+    for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
+        const int len = q4_seq_len(p, b, false);
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
-        if (tiles <= 0) continue;  // a unit that sees nothing
+        if (tiles <= 0) continue;  // a sequence that sees nothing
         at += tiles;
-        const int b = unit / p.T, tok0 = (unit - b * p.T) * p.pack;
-        const int nrows = min(p.pack, p.dense_t - tok0) * p.dense_h;
-        const long long row0 = ((long long)b * p.dense_t + tok0) * p.dense_h;
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
         auto page_of = [&](int t) { return q4_page(pt_b, p.pt_stride, p.num_pages, t); };
         auto issue = [&](int i, int pg) {  // thread 0
@@ -594,13 +589,13 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         if (tid == 0) {
             for (int t = 0; t < min(C::kStages, tiles); ++t) issue(it + t, page_of(tile0 + t));
         }
-        q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, row0, nrows);
+        q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, (long long)b * nrows, nrows);
         // visible positions of this lane's two query rows
         int lim0 = 0, lim1 = 0;
         if (w.r < nrows)
-            lim0 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + tok0 + w.r / p.dense_h), 0), p.K);
+            lim0 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + w.r / p.dense_h), 0), p.K);
         if (w.r + 8 < nrows)
-            lim1 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + tok0 + (w.r + 8) / p.dense_h), 0), p.K);
+            lim1 = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + (w.r + 8) / p.dense_h), 0), p.K);
         w.reset();
         __syncthreads();
         for (int t = 0; t < tiles; ++t, ++it) {
@@ -645,7 +640,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         __syncthreads();
         float t0, t1;
         w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1);
-        const size_t slot = (size_t)blockIdx.x + unit;
+        const size_t slot = (size_t)blockIdx.x + b;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int h = w.r + 8 * half;
@@ -671,7 +666,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
 
 // ---------------------------------------------------------------- combine of pieces
 // One CTA per query row: o = sum_c 2^(m_c - M) O_c / L, L = sum_c 2^(lse_c - M),
-// lse = M + log2 L, over the pieces c that the row's unit was cut into.
+// lse = M + log2 L, over the pieces c that the sequence was cut into.
 // 128 threads hold the 512 columns as float4; four groups of them take every
 // fourth piece and meet in shared memory.
 constexpr int kQ4CombineThreads = 512;
@@ -681,14 +676,11 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
     const PartialParams &p = a.p;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long row = blockIdx.x;  // of [B, T, H]
-    const int h = (int)(row % p.dense_h);
-    const long long tok = row / p.dense_h;
-    const int b = (int)(tok / p.dense_t), t = (int)(tok - (long long)b * p.dense_t);
-    const int unit = b * p.T + t / p.pack, r = (t % p.pack) * p.dense_h + h;
+    const int nrows = p.dense_t * p.dense_h, b = (int)(row / nrows), r = (int)(row - (long long)b * nrows);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long first = ld_input(a.prefix + unit), last = ld_input(a.prefix + unit + 1);
-    const long long total = ld_input(a.prefix + a.n_units);
+    const long long first = ld_input(a.prefix + b), last = ld_input(a.prefix + b + 1);
+    const long long total = ld_input(a.prefix + p.B);
     const int sharers = q4_sharers(a.grid, a.min_tiles, total);
     // CTA of flattened tile x: the c with total c / sharers <= x < total (c + 1) / sharers
     int c0 = 0, n = 0;
@@ -696,8 +688,8 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
         c0 = (int)(((first + 1) * sharers - 1) / total);
         n = (int)((last * sharers - 1) / total) - c0 + 1;
     }
-    const float2 *ml = a.piece_ml + ((size_t)c0 + unit) * Q4Cfg::kRows + r;
-    const float *po = a.piece_o + (((size_t)c0 + unit) * Q4Cfg::kRows + r) * kDc;
+    const float2 *ml = a.piece_ml + ((size_t)c0 + b) * Q4Cfg::kRows + r;
+    const float *po = a.piece_o + (((size_t)c0 + b) * Q4Cfg::kRows + r) * kDc;
     float M = -INFINITY;
     for (int c = tid; c < n; c += kQ4CombineThreads) M = fmaxf(M, __ldcg(ml + (size_t)c * Q4Cfg::kRows).x);
 #pragma unroll

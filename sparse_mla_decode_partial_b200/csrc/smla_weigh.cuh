@@ -15,7 +15,7 @@
 namespace smla {
 
 struct WeighParams {
-    PartialParams p;      // q, cache, pages; seq_lens [B, dense_t], K = max_n, T = 1 unit of pack = dense_t tokens
+    PartialParams p;      // q, cache, pages; seq_lens [B, dense_t], K = max_n
     const float *lse;     // [B, T, H]
     float *acc;           // [B, max_n]
     int grid;             // CTAs that share the tiles
@@ -83,12 +83,12 @@ __global__ void __launch_bounds__(WeighQ4Cfg<G>::kThreads, WeighQ4Cfg<G>::kMinBl
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Q4Run run = q4_find_run<C::kTile>(p, p.B, a.grid, a.min_tiles, nullptr,
+    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, a.min_tiles, nullptr,
                                             reinterpret_cast<int *>(smem + C::kOffScratch));
     const int rows = p.dense_t * p.dense_h;
-    int b = run.unit, tile0 = run.tile, it = 0;
+    int b = run.b, tile0 = run.tile, it = 0;
     for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
-        const int len = q4_unit_len(p, b, false);
+        const int len = q4_seq_len(p, b, false);
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;
         at += tiles;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
-    const Q4Run run = q4_find_run<64>(p, p.B, a.grid, a.min_tiles, nullptr,
+    const Q4Run run = q4_find_run<64>(p, a.grid, a.min_tiles, nullptr,
                                       reinterpret_cast<int *>(smem + C::kOffScratch));
     tc_fence_before();
     __syncthreads();
@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
     // Every role walks the same pieces (a run of one sequence's pages), passes
     // (of kMaxRows query rows) and steps (of two pages).
     auto walk = [&](auto &&body) {
-        int b = run.unit, page0 = run.tile;
+        int b = run.b, page0 = run.tile;
         for (long long at = run.begin; at < run.end; ++b, page0 = 0) {
-            const int len = q4_unit_len(p, b, false);
+            const int len = q4_seq_len(p, b, false);
             const int pages = (int)min((long long)((len + 63) / 64 - page0), run.end - at);
             if (pages <= 0) continue;
             at += pages;

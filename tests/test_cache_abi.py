@@ -45,8 +45,8 @@ def weigh(lib, q=FAKE, cache=FAKE, pages=8, pt=FAKE, stride=4, lens=FAKE, lse=FA
     return getattr(lib, name)(q, cache, pages, pt, stride, lens, lse, B, T, H, ps, scale, acc, max_n, None)
 
 
-def plan(lib, acc=FAKE, pos=FAKE, n=FAKE, B=2, max_n=100, K=50, sink=4, recent=8, ws=FAKE, wsb=BIG, src=FAKE,
-         n_new=FAKE + 4096, acc_new=FAKE + 8192, pos_new=FAKE + 8192):
+def plan(lib, acc=FAKE, pos=FAKE, n=FAKE, B=2, max_n=100, K=50, sink=4, recent=8, ws=FAKE, wsb=BIG, src=FAKE + 2048,
+         n_new=FAKE + 4096, acc_new=FAKE + 8192, pos_new=FAKE + 16384):
     return lib.smla_evict_plan(acc, pos, n, B, max_n, K, sink, recent, ws, wsb, src, n_new, acc_new, pos_new, None)
 
 
@@ -86,6 +86,8 @@ REFUSALS = [
     (plan, dict(acc=None), INVALID), (plan, dict(n_new=None), INVALID), (plan, dict(wsb=799, pos_new=None), SMALL),
     (plan, dict(ws=None, pos_new=None), INVALID), (plan, dict(ws=FAKE + 4, pos_new=None), MISALIGNED), (plan, dict(acc_new=FAKE), INVALID),
     (plan, dict(acc_new=FAKE + 796), INVALID), (plan, dict(pos_new=FAKE), INVALID), (plan, dict(n_new=FAKE + 4), INVALID),
+    (plan, dict(src=FAKE + 400), INVALID), (plan, dict(src=FAKE + 4096 - 4), INVALID), (plan, dict(acc_new=FAKE + 16384 + 796), INVALID),
+    (plan, dict(pos=FAKE + 8192 + 796), INVALID), (plan, dict(n=FAKE + 4100), INVALID),
     (plan, dict(pos=FAKE + 2), MISALIGNED),
     (apply, dict(B=-1), INVALID), (apply, dict(src=None), INVALID), (apply, dict(src=FAKE + 1), MISALIGNED),
     (apply, dict(bufs=(FAKE,) * 5, rb=(16,) * 5), UNSUPPORTED), (apply, dict(rb=(24,)), MISALIGNED),

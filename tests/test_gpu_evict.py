@@ -158,6 +158,14 @@ def test_plan_batches_and_lengths_over_the_cluster_sizes(B, most, K):
     run_plan(np.round(rng.exponential(1.0, (B, most)), 3), n, K, pos=pos, n_sink=5, n_recent=100)
 
 
+def test_plan_longest_sequences_one_thread_block_each():
+    """As many slots as a call may have, in a batch whose sequences have one block each."""
+    rng = np.random.default_rng(3)
+    n = [0] * 80
+    n[7], n[78], n[79] = 524288, 1, 300000
+    run_plan(np.round(rng.exponential(1.0, (80, 524288)), 4), n, 250000, n_recent=77)
+
+
 @pytest.mark.parametrize("kind", ["equal", "few", "zeros", "negative", "special"])
 def test_plan_ties_and_special_weights(kind):
     rng = np.random.default_rng(1)
@@ -296,6 +304,46 @@ def test_accumulate_plan_apply_in_a_graph_and_on_another_stream(q4):
         graph.replay()
         assert torch.equal(acc, want_acc) and torch.equal(cache.view(torch.uint8), want_cache.view(torch.uint8))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_pages_beyond_four_gigabytes(q4):
+    """Every operator gives the same bits over the far pages of a pool larger than
+    2^32 bytes as over a small pool."""
+    far = 170000 if q4 else 60000
+    lens = [300, 129]
+    paged = cu.Paged(lens, 5)
+    small, _ = make_cache(paged, q4, 6)
+    big = torch.empty(far, *small.shape[1:], dtype=small.dtype, device="cuda")
+    shift = far - paged.pages
+    big[shift:] = small
+    assert shift * small[0].numel() * small.element_size() > 2 ** 32
+    near = paged.cuda
+    table = torch.where(near >= 0, near + shift, near)
+    q = cu.queries(2, 1, 16, 7).cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    seq, lse = n[:, None].contiguous(), torch.full((2, 1, 16), 6.0).cuda()
+    rows = cu.latents(9, 8).cuda()
+    got = []
+    for cache, pt in ((small, near), (big, table)):
+        out = []
+        if q4:
+            binding.q4_append(rows, cache, pt, torch.tensor([0, 4, 9], dtype=torch.int32).cuda(), n - 5)
+            every = torch.arange(300, dtype=torch.int32).expand(2, 300).cuda().where(torch.arange(300).cuda() < n[:, None], -1)
+            idx = every.int().contiguous()
+            out.append(binding.q4_read(cache, pt, idx))
+            for H in (16, 40):
+                qh = cu.queries(2, 1, H, 9).cuda()
+                out.extend(binding.decode_q4(qh, cache, pt, idx[:, None], SCALE))
+                out.extend(binding.decode_dense_q4(qh, cache, pt, seq, SCALE, K=300))
+        acc = torch.zeros(2, 300).cuda()
+        out.append(binding.evict_accumulate(q, cache, pt, seq, lse, SCALE, acc))
+        p = binding.evict_plan(acc, n, 100)
+        out.extend(p)
+        binding.evict_apply(p.src, pt, (cache,))
+        got.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(big[shift:].view(torch.uint8), small.view(torch.uint8))
 
 
 # ---------------------------------------------------------------- together
