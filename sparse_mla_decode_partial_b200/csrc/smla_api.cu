@@ -1218,7 +1218,6 @@ int q4_sparse_nsplit(long long bt, int K, int sms) {
 }
 
 // The dense schedule of sequences with at most kQ4Rows query rows in all.
-constexpr int kQ4MinTiles = 2;
 bool q4_dense_small(int T, int H) { return (long long)T * H <= kQ4Rows; }
 struct Q4Dense {
     long long ctas;
@@ -1381,7 +1380,6 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
         a.p.o = static_cast<__nv_bfloat16 *>(o);
         a.p.lse = lse;
         a.grid = (int)d.ctas;
-        a.min_tiles = kQ4MinTiles;
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         a.piece_o = reinterpret_cast<float *>(ws);
         a.piece_ml = reinterpret_cast<float2 *>(ws + d.off_ml);
@@ -1391,7 +1389,10 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
         if (e != cudaSuccess) return cuda_fail(e);
         e = launch_dependent(smla::smla_q4_dense_kernel, a.grid, C::kThreads, C::kSmemBytes, s, a);
         if (e != cudaSuccess) return cuda_fail(e);
-        e = launch_dependent(smla::smla_q4_combine_kernel, B * T * H, smla::kQ4CombineThreads, 0, s, a);
+        const int rows = B * T * H;
+        e = rows <= current_device_sms() / 2
+                ? launch_dependent(smla::smla_q4_combine_kernel<4>, 4 * rows, smla::kQ4CombineThreads, 0, s, a)
+                : launch_dependent(smla::smla_q4_combine_kernel<1>, rows, smla::kQ4CombineThreads, 0, s, a);
         return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
     }
     DensePlan d = dense_plan(B, T, H, K, nsplit);
@@ -1461,7 +1462,6 @@ smla_status launch_weigh_bf16(smla::WeighParams &a, cudaStream_t st) {
     if (e != cudaSuccess) return cuda_fail(e);
     const long long pages = a.p.B * (((long long)a.p.K + 63) / 64);
     a.grid = (int)std::min<long long>(pages, current_device_sms());
-    a.min_tiles = 2;
     e = launch_dependent(smla::smla_weigh_bf16_kernel, a.grid, C::kThreads, C::kSmemBytes, st, map_kv, map_q, a);
     return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
@@ -1473,7 +1473,6 @@ cudaError_t launch_weigh_q4(smla::WeighParams &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const long long tiles = a.p.B * (((long long)a.p.K + C::kTile - 1) / C::kTile);
     a.grid = (int)std::min<long long>(tiles, (long long)C::kMinBlocks * current_device_sms());
-    a.min_tiles = 2;
     return launch_dependent(smla::smla_weigh_q4_kernel<G>, a.grid, C::kThreads, C::kSmemBytes, st, a);
 }
 

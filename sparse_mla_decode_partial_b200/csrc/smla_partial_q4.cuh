@@ -60,7 +60,6 @@ static_assert(Q4Cfg::kMinBlocks * (Q4Cfg::kSmemBytes + 1024) <= 233472, "shared 
 struct Q4Params {
     PartialParams p;   // dense_t tokens of dense_h heads, at most 16 rows together
     int grid;          // CTAs that share the tiles
-    int min_tiles;     // fewest tiles worth a CTA
     int *prefix;       // [B + 1] tiles before each sequence, written by CTA 0
     float *piece_o;    // [grid + B, 16, 512]
     float2 *piece_ml;  // [grid + B, 16]: (max, lse) in log2 units
@@ -482,28 +481,29 @@ __device__ __forceinline__ int q4_seq_len(const PartialParams &p, int b, bool co
     return len;
 }
 
-// CTAs that share `total` tiles.
+// CTAs that share `total` tiles, min_tiles or more each.
 __host__ __device__ __forceinline__ int q4_sharers(int grid, int min_tiles, long long total) {
     const long long most = (total + min_tiles - 1) / min_tiles;
     return (int)(most < 1 ? 1 : most < grid ? most : grid);
 }
 
 // A CTA's run [begin, end) of the flattened tiles of TILE positions: total
-// first, then the sequence and the tile it starts in.  Every thread calls it;
+// first, then the sequence (b, of length len) and the tile it starts in.  Every thread calls it;
 // scratch holds 48 ints of shared memory.  The first CTA counts bad lengths.
 struct Q4Run {
     long long total, begin, end;
-    int b, tile;
+    int b, len, tile;
 };
 template <int TILE>
 __device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int grid, int min_tiles, int *prefix,
                                              int *scratch) {
     const bool first_cta = blockIdx.x == 0;
     Q4Run r{};
-    int tiles = 0, incl = 0, sum = 0;
+    int len = 0, tiles = 0, incl = 0, sum = 0;
     for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
-        tiles = b < p.B ? (q4_seq_len(p, b, first_cta) + TILE - 1) / TILE : 0;
+        len = b < p.B ? q4_seq_len(p, b, first_cta) : 0;
+        tiles = (len + TILE - 1) / TILE;
         incl = ix_block_scan(tiles, scratch, &sum);
         if (prefix != nullptr && first_cta && b < p.B) prefix[b] = (int)r.total + incl - tiles;
         r.total += sum;
@@ -517,19 +517,22 @@ __device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int grid, i
     for (int b0 = 0; b0 < p.B && before <= r.begin; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         if (p.B > (int)blockDim.x) {  // else the counts above are still those of this chunk
-            tiles = b < p.B ? (q4_seq_len(p, b, false) + TILE - 1) / TILE : 0;
+            len = b < p.B ? q4_seq_len(p, b, false) : 0;
+            tiles = (len + TILE - 1) / TILE;
             incl = ix_block_scan(tiles, scratch, &sum);
         }
         const long long first = before + incl - tiles;
         if (first <= r.begin && r.begin < first + tiles) {
             scratch[40] = b;
             scratch[41] = (int)(r.begin - first);
+            scratch[42] = len;
         }
         before += sum;
     }
     __syncthreads();
     r.b = scratch[40];
     r.tile = scratch[41];
+    r.len = scratch[42];
     return r;
 }
 
@@ -568,14 +571,14 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, a.min_tiles, a.prefix, scratch);
+    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, 1, a.prefix, scratch);
     const int nrows = p.dense_t * p.dense_h;
     int b = run.b, tile0 = run.tile;
     Q4Consumer w;
     w.init(warp, lane);
     int it = 0;
     for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
-        const int len = q4_seq_len(p, b, false);
+        const int len = q4_seq_len(p, b, false);  // (run.len in a register through the loop: 110.6 us where this takes 108.4)
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;  // a sequence that sees nothing
         at += tiles;
@@ -665,23 +668,28 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
 }
 
 // ---------------------------------------------------------------- combine of pieces
-// One CTA per query row: o = sum_c 2^(m_c - M) O_c / L, L = sum_c 2^(lse_c - M),
-// lse = M + log2 L, over the pieces c that the sequence was cut into.
-// 128 threads hold the 512 columns as float4; four groups of them take every
-// fourth piece and meet in shared memory.
+// For each query row o = sum_c 2^(m_c - M) O_c / L, L = sum_c 2^(lse_c - M),
+// lse = M + log2 L, over the pieces c that the sequence was cut into.  PARTS
+// CTAs per row share its 512 columns: 128 / PARTS threads hold a CTA's columns
+// as float4, and 4 PARTS groups of them take every (4 PARTS)-th piece and meet
+// in shared memory.
 constexpr int kQ4CombineThreads = 512;
+template <int PARTS>
 __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(const Q4Params a) {
-    __shared__ float4 part[3][128];
-    __shared__ float warp_max[16], warp_sum[16];
+    constexpr int kCols = 128 / PARTS, kGroups = kQ4CombineThreads / kCols;
+    __shared__ float4 part[kGroups - 1][kCols];
+    __shared__ float warp_max[16], warp_sum[16], weight[kQ4CombineThreads];
+    constexpr int kAhead = 4;
     const PartialParams &p = a.p;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long row = blockIdx.x;  // of [B, T, H]
+    const long long row = blockIdx.x / PARTS;  // of [B, T, H]
+    const int col0 = blockIdx.x % PARTS * kCols;
     const int nrows = p.dense_t * p.dense_h, b = (int)(row / nrows), r = (int)(row - (long long)b * nrows);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long first = ld_input(a.prefix + b), last = ld_input(a.prefix + b + 1);
     const long long total = ld_input(a.prefix + p.B);
-    const int sharers = q4_sharers(a.grid, a.min_tiles, total);
+    const int sharers = q4_sharers(a.grid, 1, total);
     // CTA of flattened tile x: the c with total c / sharers <= x < total (c + 1) / sharers
     int c0 = 0, n = 0;
     if (last > first) {
@@ -690,8 +698,20 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
     }
     const float2 *ml = a.piece_ml + ((size_t)c0 + b) * Q4Cfg::kRows + r;
     const float *po = a.piece_o + (((size_t)c0 + b) * Q4Cfg::kRows + r) * kDc;
-    float M = -INFINITY;
-    for (int c = tid; c < n; c += kQ4CombineThreads) M = fmaxf(M, __ldcg(ml + (size_t)c * Q4Cfg::kRows).x);
+    // The first loads of the pieces go out beside those of their maxima.
+    const int g = tid / kCols, col = tid % kCols;
+    auto piece = [&](int c) {
+        return c < n ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)c * Q4Cfg::kRows * kDc) + col0 + col)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ahead[k] = piece(g + k * kGroups);
+    const float2 none = make_float2(-INFINITY, -INFINITY);
+    auto max_lse = [&](int c) { return c < n ? __ldcg(ml + (size_t)c * Q4Cfg::kRows) : none; };
+    const float2 mine = max_lse(tid);
+    float M = mine.x;
+    for (int c = tid + kQ4CombineThreads; c < n; c += kQ4CombineThreads) M = fmaxf(M, max_lse(c).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) warp_max[warp] = M;
@@ -701,31 +721,33 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
     for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     __nv_bfloat16 *out = p.o + row * kDc;
     if (M == -INFINITY) {  // nothing attended to
-        if (tid < 128) *reinterpret_cast<uint2 *>(out + 4 * tid) = make_uint2(0u, 0u);
-        if (tid == 0) p.lse[row] = -INFINITY;
+        if (tid < kCols) *reinterpret_cast<uint2 *>(out + 4 * (col0 + tid)) = make_uint2(0u, 0u);
+        if (tid == 0 && col0 == 0) p.lse[row] = -INFINITY;
         return;
     }
-    float L = 0.f;
-    for (int c = tid; c < n; c += kQ4CombineThreads) {
-        const float v = __ldcg(ml + (size_t)c * Q4Cfg::kRows).y;
+    weight[tid] = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);  // 0: an empty piece, or none
+    float L = mine.y == -INFINITY ? 0.f : exp2f(mine.y - M);
+    for (int c = tid + kQ4CombineThreads; c < n; c += kQ4CombineThreads) {
+        const float v = max_lse(c).y;
         if (v != -INFINITY) L += exp2f(v - M);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) warp_sum[warp] = L;
-    const int g = tid >> 7, col = tid & 127;
+    __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = g; c < n; c += 4) {
-        const float m = __ldcg(ml + (size_t)c * Q4Cfg::kRows).x;
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(po + (size_t)c * Q4Cfg::kRows * kDc) + col);
-        if (m == -INFINITY) continue;  // an empty piece
-        const float f = exp2f(m - M);
+    auto add = [&](int c, const float4 &v) {
+        const float f = c < kQ4CombineThreads ? weight[c] : exp2f(max_lse(c).x - M);
+        if (f == 0.f) return;  // (what an empty piece holds is undefined)
         acc.x += f * v.x;
         acc.y += f * v.y;
         acc.z += f * v.z;
         acc.w += f * v.w;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) add(min(g + k * kGroups, kQ4CombineThreads - 1), ahead[k]);
+#pragma unroll 4
+    for (int c = g + kAhead * kGroups; c < n; c += kGroups) add(c, piece(c));
     if (g > 0) part[g - 1][col] = acc;
     __syncthreads();
     if (g > 0) return;
@@ -733,7 +755,7 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
 #pragma unroll
     for (int w = 0; w < 16; ++w) L += warp_sum[w];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < kGroups - 1; ++k) {
         const float4 v = part[k][col];
         acc.x += v.x;
         acc.y += v.y;
@@ -741,9 +763,9 @@ __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(cons
         acc.w += v.w;
     }
     const float inv = 1.f / L;
-    *reinterpret_cast<uint2 *>(out + 4 * col) =
+    *reinterpret_cast<uint2 *>(out + 4 * (col0 + col)) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (tid == 0) p.lse[row] = (M + log2f(L)) * kLn2;
+    if (tid == 0 && col0 == 0) p.lse[row] = (M + log2f(L)) * kLn2;
 }
 
 }  // namespace smla

@@ -19,7 +19,6 @@ struct WeighParams {
     const float *lse;     // [B, T, H]
     float *acc;           // [B, max_n]
     int grid;             // CTAs that share the tiles
-    int min_tiles;        // fewest tiles worth a CTA
 };
 
 // Query row r of sequence b: lse in log2 units as a sum of two floats (its
@@ -83,12 +82,12 @@ __global__ void __launch_bounds__(WeighQ4Cfg<G>::kThreads, WeighQ4Cfg<G>::kMinBl
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, a.min_tiles, nullptr,
+    const Q4Run run = q4_find_run<C::kTile>(p, a.grid, 1, nullptr,
                                             reinterpret_cast<int *>(smem + C::kOffScratch));
     const int rows = p.dense_t * p.dense_h;
     int b = run.b, tile0 = run.tile, it = 0;
     for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
-        const int len = q4_seq_len(p, b, false);
+        const int len = at == run.begin ? run.len : q4_seq_len(p, b, false);
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;
         at += tiles;
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
-    const Q4Run run = q4_find_run<64>(p, a.grid, a.min_tiles, nullptr,
+    const Q4Run run = q4_find_run<64>(p, a.grid, 2, nullptr,
                                       reinterpret_cast<int *>(smem + C::kOffScratch));
     tc_fence_before();
     __syncthreads();
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
     auto walk = [&](auto &&body) {
         int b = run.b, page0 = run.tile;
         for (long long at = run.begin; at < run.end; ++b, page0 = 0) {
-            const int len = q4_seq_len(p, b, false);
+            const int len = at == run.begin ? run.len : q4_seq_len(p, b, false);
             const int pages = (int)min((long long)((len + 63) / 64 - page0), run.end - at);
             if (pages <= 0) continue;
             at += pages;
