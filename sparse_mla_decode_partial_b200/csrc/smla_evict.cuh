@@ -144,10 +144,13 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
             for (int i = lo + tid; i < hi; i += kPlanThreads)
                 if (safe(i)) keys[i - lo] = 0xFFFFFFFFu;
         }
-        cluster_sync();  // the cleared sums too
+        if (p.pos == nullptr)
+            cluster_sync();  // the sums are cleared (with pos, the exchange above saw to that)
+        else
+            __syncthreads();
 
         uint32_t prefix = 0;  // the K-th largest key, digit by digit
-        int need = p.K;
+        int need = p.K, equal_all = 0;
 #pragma unroll 1
         for (int digit = 0; digit < 3; ++digit) {
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
@@ -184,12 +187,15 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
                     const bool first = excl + (int)h1 >= need;
                     dec[0] = kPlanBins - (first ? 1 : 2) - 2 * tid;
                     dec[1] = need - excl - (first ? 0 : (int)h1);
+                    dec[2] = (int)(first ? h1 : h0);
                 }
             }
             cluster_sync();
             prefix |= ld_cluster(&dec[0], 0) << shift;
             need = (int)ld_cluster(&dec[1], 0);
+            equal_all = (int)ld_cluster(&dec[2], 0);
         }
+        const bool split = need < equal_all;  // not all slots at the K-th key stay
 
         // bitmaps: slots above the K-th key, slots equal to it
         const int nw = hi > lo ? (hi - lo + 31) / 32 : 0;
@@ -200,36 +206,37 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
             const uint32_t above = __ballot_sync(0xffffffffu, i < hi && k > prefix);
             const uint32_t equal = __ballot_sync(0xffffffffu, i < hi && k == prefix);
             if (lane == 0) {
-                keep[w] = above;
+                keep[w] = split ? above : above | equal;
                 tie[w] = equal;
                 equal_here += __popc(equal);
             }
         }
-        if (lane == 0) scratch[warp] = equal_here;
-        __syncthreads();
-        if (warp == 0) {
-            const int x = __reduce_add_sync(0xffffffffu, scratch[lane]);
-            if (lane == 0) xch[1] = x;
-        }
-        cluster_sync();
-        // the first `need` ties stay
-        int carry = 0;
-        for (uint32_t r = 0; r < rank; ++r) carry += (int)ld_cluster(&xch[1], r);
-        for (int w0 = 0; w0 < nw; w0 += kPlanThreads) {
-            const int w = w0 + tid;
-            const uint32_t t = w < nw ? tie[w] : 0u;
-            int total;
-            const int incl = ix_block_scan(__popc(t), scratch, &total);
-            const int before = carry + incl - __popc(t);
-            if (w < nw) {
-                uint32_t left = t, got = 0u;
-                for (int k = before; k < need && left; ++k) {
-                    got |= left & (0u - left);
-                    left &= left - 1u;
-                }
-                keep[w] |= got;
+        if (split) {  // the first `need` of them do
+            if (lane == 0) scratch[warp] = equal_here;
+            __syncthreads();
+            if (warp == 0) {
+                const int x = __reduce_add_sync(0xffffffffu, scratch[lane]);
+                if (lane == 0) xch[1] = x;
             }
-            carry += total;
+            cluster_sync();
+            int carry = 0;
+            for (uint32_t r = 0; r < rank; ++r) carry += (int)ld_cluster(&xch[1], r);
+            for (int w0 = 0; w0 < nw; w0 += kPlanThreads) {
+                const int w = w0 + tid;
+                const uint32_t t = w < nw ? tie[w] : 0u;
+                int total;
+                const int incl = ix_block_scan(__popc(t), scratch, &total);
+                const int before = carry + incl - __popc(t);
+                if (w < nw) {
+                    uint32_t left = t, got = 0u;
+                    for (int k = before; k < need && left; ++k) {
+                        got |= left & (0u - left);
+                        left &= left - 1u;
+                    }
+                    keep[w] |= got;
+                }
+                carry += total;
+            }
         }
         __syncthreads();
         // movers (slots at or behind m that stay) and holes (slots before m
@@ -274,14 +281,6 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
         cluster_sync();  // the movers' list and pre are complete; no CTA leaves while another reads its counts
     }
     // this CTA's slots below m, then its share of what lies behind
-    auto put = [&](int i, int s) {
-        if (i < p.K) src[i] = s;
-        if (i < p.max_n) {
-            if (p.acc_new != nullptr) p.acc_new[base + i] = s < 0 ? 0.f : ld_weight(p.acc + base + s);
-            if (p.pos_new != nullptr)
-                p.pos_new[base + i] = s < 0 ? -1 : p.pos != nullptr ? ld_input(p.pos + base + s) : s;
-        }
-    };
 #pragma unroll 4
     for (int i = lo + tid; i < min(hi, m); i += kPlanThreads) {
         int s = i;
@@ -292,11 +291,19 @@ __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const Evi
                 s = ld_input(movers + pre[(i - lo) >> 5] + __popc(~k & lower));
             }
         }
-        put(i, s);
+        src[i] = s;
+        if (p.acc_new != nullptr) p.acc_new[base + i] = ld_weight(p.acc + base + s);
+        if (p.pos_new != nullptr) p.pos_new[base + i] = p.pos != nullptr ? ld_input(p.pos + base + s) : s;
     }
+    // (no stores before this barrier that need not be: it waits for them; with
+    // those of acc_new and src ahead of it 16 sequences took 41 us, not 26)
     if (cut) cluster_sync();  // the movers have been read
-    for (long long i = m + (long long)rank * kPlanThreads + tid; i < max(p.K, p.max_n); i += nc * kPlanThreads)
-        put((int)i, -1);
+    for (long long i = m + (long long)rank * kPlanThreads + tid; i < max(p.K, p.max_n); i += nc * kPlanThreads) {
+        if (i < p.K) src[i] = -1;
+        if (i >= p.max_n) continue;
+        if (p.acc_new != nullptr) p.acc_new[base + i] = 0.f;
+        if (p.pos_new != nullptr) p.pos_new[base + i] = -1;
+    }
 }
 
 // ---------------------------------------------------------------- apply
