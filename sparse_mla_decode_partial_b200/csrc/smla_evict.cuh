@@ -80,6 +80,8 @@ __device__ __forceinline__ float ld_weight(const float *p) {
 // summed in the first CTA), bitmaps of the slots above and at it, ties to the
 // smaller slot, then ranks of holes and movers by prefix sums.  A handful of
 // block and cluster barriers with little work between them: latency bounds it.
+// Measured: 8448 slots 17.7 us, 16 sequences of 12132 to 29815 slots 25.0 us
+// (with one CTA a sequence 23.6 and 46.5).
 __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const EvictPlanParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int words = p.per / 32;

@@ -26,6 +26,15 @@
 // Rows 416 bytes apart: the lane-to-row map below keeps every shared load free
 // of bank conflicts without padding, so a page of the cache lands by one bulk
 // copy.
+// What bounds it: per 64-row tile an SM quarter spends about 1090 cycles on its
+// 136 products (eight each) and 970 on the integer half of decoding, and the two
+// hardly overlap: 2080 cycles in all with everything resident, 2450 in a full
+// launch (issue slots 49% taken, integer pipe 43%, tensor pipe 37%, shared memory
+// 42%).  Measured with the combine: 32 sequences of 4329 to 65378 positions, 16
+// heads, 108.5 us (2.4 TB/s of rows; 40 us at the memory's rate); 64 lists of
+// 2048 rows 36.8 us; one list 8.7 us.  Slower: eight warps a tile (137 us for the
+// first), one CTA of three groups per SM and a ring of seven pages (124), the
+// score half on tcgen05 with rows decoded into tensor memory (181).
 #pragma once
 
 #include <cstdint>
@@ -122,34 +131,27 @@ __device__ __forceinline__ uint32_t bf16x2_pow2(float d) {
     return (uint32_t)(e << 7) * 0x00010001u;
 }
 
-// Raw scores of 16 cache rows (those at `rows`, 416 bytes apart) against 16 G
-// query rows, whose A fragments are uint4 [36][G][32] at q.  s[g][i]: query rows
-// 16 g + r, + 8 against columns 2 c, 2 c + 1 of the i-th n8 tile.  Each fragment
-// of the cache is decoded once for all G.
-template <int G>
-__device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, float (&s)[G][2][4]) {
+// Raw scores of 16 cache rows (those at `rows`, 416 bytes apart) against the 16
+// query rows, whose A fragments are uint4 [36][32] at q.  s[i]: query rows r,
+// r + 8 against columns 2 c, 2 c + 1 of the i-th n8 tile.
+__device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, float (&s)[2][4]) {
     const int c = lane & 3;
     const uint32_t row = rows + q4_row_of(lane >> 2) * kQ4RowBytes;
     q += 16 * lane;
-    // With one group, even and odd steps keep accumulators of their own: two
-    // chains of 36 dependent products left the pipe waiting for their latency.
-    constexpr int kOdd = G == 1 ? 1 : 0;
+    // Even and odd steps keep accumulators of their own: two chains of 36
+    // dependent products left the pipe waiting for their latency.
     float odd[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         odd[i][0] = odd[i][1] = odd[i][2] = odd[i][3] = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g) s[g][i][0] = s[g][i][1] = s[g][i][2] = s[g][i][3] = 0.f;
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
     }
     auto steps = [&](int st, const uint4 (&v)[2]) {  // k16 steps st, st + 1
+        const uint4 a0 = lds_16(q + st * 512), a1 = lds_16(q + (st + 1) * 512);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const uint4 a0 = lds_16(q + (st * G + g) * 512), a1 = lds_16(q + ((st + 1) * G + g) * 512);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mma_bf16_16816(s[g][i], a0.x, a0.y, a0.z, a0.w, v[i].x, v[i].y);
-                mma_bf16_16816(kOdd ? odd[i] : s[g][i], a1.x, a1.y, a1.z, a1.w, v[i].z, v[i].w);
-            }
+        for (int i = 0; i < 2; ++i) {
+            mma_bf16_16816(s[i], a0.x, a0.y, a0.z, a0.w, v[i].x, v[i].y);
+            mma_bf16_16816(odd[i], a1.x, a1.y, a1.z, a1.w, v[i].z, v[i].w);
         }
     };
 #pragma unroll
@@ -180,12 +182,10 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
         for (int i = 0; i < 2; ++i) v[i] = lds_16(row + i * 8 * kQ4RowBytes + kQ4OffRope + 64 * j + 16 * c);
         steps(32 + 2 * j, v);
     }
-    if (kOdd) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[0][i][k] += odd[i][k];
-    }
+        for (int k = 0; k < 4; ++k) s[i][k] += odd[i][k];
 }
 
 // One warp's share of a CTA: scores of 16 rows, 128 output columns.
@@ -325,14 +325,14 @@ struct Q4Consumer {
     }
 };
 
-// Stage 16 G query rows (row0 .. row0 + nrows - 1 of q; the rest zero) as A
+// Stage 16 query rows (row0 .. row0 + nrows - 1 of q; the rest zero) as A
 // fragments in lane order, by NT threads.
-template <int G, int NT>
+template <int NT>
 __device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q, long long row0, int nrows) {
     uint4 *frag = reinterpret_cast<uint4 *>(dst);
 #pragma unroll
-    for (int k = 0; k < 36 * G * 32 / NT; ++k) {
-        const int i = threadIdx.x + NT * k, l = i & 31, g = (i >> 5) % G, st = i / (32 * G), r = 16 * g + (l >> 2);
+    for (int k = 0; k < 36 * 32 / NT; ++k) {
+        const int i = threadIdx.x + NT * k, l = i & 31, st = i >> 5, r = l >> 2;
         const __nv_bfloat16 *src = q + (row0 + r) * kD + q4_dim_of(st, l & 3);
         uint2 lo = make_uint2(0u, 0u), hi = lo;
         if (r < nrows)
@@ -345,7 +345,12 @@ __device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q,
 
 // ---------------------------------------------------------------- sparse lists
 // One CTA = one (query token, split).  Equal splits; the partials go to
-// part_o / part_m / part_lse [B, T, H, S] (DIRECT: o, lse).
+// part_o / part_m / part_lse [B, T, H, S] (DIRECT: o, lse).  Rows come by 16-byte
+// cp.async (64 lists of 2048: 37 us; by one bulk copy a row 39.6).  Equal runs over
+// the batch as in the dense schedule took 47 us: a run that goes on in the next
+// list starts its pipeline anew.  A cluster of four splits that merge in
+// distributed shared memory took 35.8, but of two 60.8 against 43.7 and of sixteen
+// (15 lists) 23.5 against 14.9.
 template <bool DIRECT>
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sparse_kernel(const PartialParams p) {
     using C = Q4Cfg;
@@ -396,16 +401,15 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
         const int tiles = (n + C::kTile - 1) / C::kTile;
         for (int t = 0; t < min(C::kStages, tiles); ++t) issue(it + t, t, n);
         if (!staged) {
-            q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
+            q4_stage_q<C::kThreads>(smem + C::kOffQ, p.q, (long long)bt * p.H, p.H);
             staged = true;
             __syncthreads();
         }
         for (int t = 0; t < tiles; ++t, ++it) {
             const uint32_t tile = sbase + C::kOffStage + it % C::kStages * C::kStageBytes;
             mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1, dead);
-            float sg[1][2][4];
-            q4_scores<1>(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sg);
-            float (&sc)[2][4] = sg[0];
+            float sc[2][4];
+            q4_scores(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sc);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         if (tid == 0) {
             for (int t = 0; t < min(C::kStages, tiles); ++t) issue(it + t, page_of(tile0 + t));
         }
-        q4_stage_q<1, C::kThreads>(smem + C::kOffQ, p.q, (long long)b * nrows, nrows);
+        q4_stage_q<C::kThreads>(smem + C::kOffQ, p.q, (long long)b * nrows, nrows);
         // visible positions of this lane's two query rows
         int lim0 = 0, lim1 = 0;
         if (w.r < nrows)
@@ -620,9 +624,8 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
                 }
                 __syncthreads();
             }
-            float sg[1][2][4];
-            q4_scores<1>(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sg);
-            float (&sc)[2][4] = sg[0];
+            float sc[2][4];
+            q4_scores(sbase + C::kOffQ, tile + 16 * warp * kQ4RowBytes, lane, sc);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -672,7 +675,10 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
 // lse = M + log2 L, over the pieces c that the sequence was cut into.  PARTS
 // CTAs per row share its 512 columns: 128 / PARTS threads hold a CTA's columns
 // as float4, and 4 PARTS groups of them take every (4 PARTS)-th piece and meet
-// in shared memory.
+// in shared memory.  PARTS is 4 while rows are at most half the SMs.  With 4 and
+// with 1 (both kernels): one sequence of 37888 positions, 16 rows, 18.1 and 24.8
+// us; four of 64000, 64 rows, 51.4 and 52.8; five of 51200, 80 rows, 54.9 and
+// 54.1; nine of 19200, 144 rows, 43.3 and 41.8.
 constexpr int kQ4CombineThreads = 512;
 template <int PARTS>
 __global__ void __launch_bounds__(kQ4CombineThreads) smla_q4_combine_kernel(const Q4Params a) {

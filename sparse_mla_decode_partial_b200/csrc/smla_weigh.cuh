@@ -39,45 +39,41 @@ __device__ __forceinline__ void weigh_row(const WeighParams &a, int b, int r, fl
         *lim = min(max(ld_input(p.seq_lens + (size_t)b * p.dense_t + r / p.dense_h), 0), p.K);
 }
 
-// ---------------------------------------------------------------- 4-bit rows
+// ---------------------------------------------------------------- 4-bit rows, up to 16 query rows
 // The dense decode's schedule and score product (smla_partial_q4.cuh): CTAs take
 // equal runs of the batch's 64-position tiles, a page lands by one bulk copy,
-// and each warp scores 16 of its rows against 16 G query rows at a time,
-// decoding the codes once.  More query rows than 16 G go in further passes over
-// the run's tiles by the same threads, so that every position is added to in a
-// fixed order.
-template <int G>
+// and each warp scores 16 of its rows against the 16 query rows.  Measured: 24
+// sequences of 4635 to 64913 positions, 16 heads, 51.9 us (4.6 TB/s; 36 us at the
+// memory's rate; 70.9 by the kernel below): 0.72 us a page and SM in steady state,
+// 0.6 of it the bytes' time; shared memory is 53% busy.
 struct WeighQ4Cfg {
-    static constexpr int kWarps = G == 4 ? 8 : 4;          // G = 4: one CTA per SM, so more warps in it
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kPages = kWarps / 4;              // pages of a tile
-    static constexpr int kTile = 64 * kPages;
+    static constexpr int kThreads = 128;
+    static constexpr int kTile = 64;                       // one page
     static constexpr int kStages = 2;
-    static constexpr int kStageBytes = kPages * Q4Cfg::kStageBytes;
+    static constexpr int kStageBytes = Q4Cfg::kStageBytes;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffStage = 36 * G * 512;
-    static constexpr int kOffRow = kOffStage + kStages * kStageBytes;  // float2 lse [16 G], int lim [16 G]
-    static constexpr int kOffScratch = kOffRow + 16 * G * 12;          // int [48]
+    static constexpr int kOffStage = 36 * 512;
+    static constexpr int kOffRow = kOffStage + kStages * kStageBytes;  // float2 lse [16], int lim [16]
+    static constexpr int kOffScratch = kOffRow + 16 * 12;          // int [48]
     static constexpr int kOffBar = kOffScratch + 192;
     static constexpr int kSmemBytes = kOffBar + 8 * kStages;
-    static constexpr int kMinBlocks = G == 1 ? 3 : G == 2 ? 2 : 1;     // per SM
+    static constexpr int kMinBlocks = 3;                   // per SM
     static_assert(kMinBlocks * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
 
-template <int G>
-__global__ void __launch_bounds__(WeighQ4Cfg<G>::kThreads, WeighQ4Cfg<G>::kMinBlocks)
+__global__ void __launch_bounds__(WeighQ4Cfg::kThreads, WeighQ4Cfg::kMinBlocks)
     smla_weigh_q4_kernel(const WeighParams a) {
-    using C = WeighQ4Cfg<G>;
+    using C = WeighQ4Cfg;
     const PartialParams &p = a.p;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x, c = lane & 3, r = lane >> 2;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
     float2 *lse_s = reinterpret_cast<float2 *>(smem + C::kOffRow);
-    int *lim_s = reinterpret_cast<int *>(lse_s + 16 * G);
+    int *lim_s = reinterpret_cast<int *>(lse_s + 16);
     const uint32_t sbase = smem_addr(smem);
     bool dead = false;
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], C::kPages);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -93,81 +89,93 @@ __global__ void __launch_bounds__(WeighQ4Cfg<G>::kThreads, WeighQ4Cfg<G>::kMinBl
         at += tiles;
         const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
         float *acc = a.acc + (size_t)b * p.K;
-        auto page_of = [&](int pg) { return pg * 64 < len ? q4_page(pt_b, p.pt_stride, p.num_pages, pg) : -1; };
-        auto issue = [&](int i, int t) {  // thread 0: tile t of the sequence into ring position i
-#pragma unroll
-            for (int k = 0; k < C::kPages; ++k)
-                q4_copy_page(p, page_of(C::kPages * t + k),
-                             smem + C::kOffStage + (i & 1) * C::kStageBytes + k * Q4Cfg::kStageBytes, &full[i & 1]);
+        auto page_of = [&](int t) { return q4_page(pt_b, p.pt_stride, p.num_pages, tile0 + t); };
+        auto issue = [&](int i, int t) {  // thread 0: tile t of the run into ring position i
+            q4_copy_page(p, page_of(t), smem + C::kOffStage + (i & 1) * C::kStageBytes, &full[i & 1]);
         };
-        for (int g0 = 0; g0 < rows; g0 += 16 * G) {
-            __syncthreads();  // the previous pass is done with the ring, Q and the row data
-            if (tid == 0) {
-                issue(it, tile0);
-                if (tiles > 1) issue(it + 1, tile0 + 1);
+        __syncthreads();  // the previous sequence is done with the ring, Q and the row data
+        if (tid == 0) {
+            issue(it, 0);
+            if (tiles > 1) issue(it + 1, 1);
+        }
+        q4_stage_q<C::kThreads>(smem + C::kOffQ, p.q, (long long)b * rows, rows);
+        if (tid < 16) weigh_row(a, b, tid, &lse_s[tid], &lim_s[tid]);
+        __syncthreads();
+        for (int t = 0; t < tiles; ++t, ++it) {
+            // lane (r, c), r < 4, adds up column 2 c + (r & 1) of n8 tile r >> 1
+            const int pos0 = (tile0 + t) * 64 + 16 * warp;
+            const bool mapped = page_of(t) >= 0;
+            const int pos = pos0 + 8 * (r >> 1) + q4_row_of(2 * c + (r & 1));
+            const bool mine = r < 4 && mapped && pos < len;
+            float old = 0.f;
+            if (mine) asm volatile("ld.global.f32 %0, [%1];" : "=f"(old) : "l"(acc + pos));
+            mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
+            float s[2][4];
+            q4_scores(sbase + C::kOffQ,
+                      sbase + C::kOffStage + (it & 1) * C::kStageBytes + 16 * warp * kQ4RowBytes, lane, s);
+            __syncthreads();  // every warp is done with the tile
+            if (tid == 0 && t + 2 < tiles) issue(it + 2, t + 2);
+            if (!mapped) {
+                if (lane < min(len - pos0, 16)) count_bad_index();
+                continue;
             }
-            q4_stage_q<G, C::kThreads>(smem + C::kOffQ, p.q, (long long)b * rows + g0, rows - g0);
-            if (tid < 16 * G) weigh_row(a, b, g0 + tid, &lse_s[tid], &lim_s[tid]);
-            __syncthreads();
-            for (int t = 0; t < tiles; ++t, ++it) {
-                // lane (r, c), r < 4, adds up column 2 c + (r & 1) of n8 tile r >> 1
-                const int page = C::kPages * (tile0 + t) + (warp >> 2);
-                const int pos0 = page * 64 + 16 * (warp & 3);
-                const bool mapped = page_of(page) >= 0;
-                const int pos = pos0 + 8 * (r >> 1) + q4_row_of(2 * c + (r & 1));
-                const bool mine = r < 4 && mapped && pos < len;
-                float old = 0.f;
-                if (mine) asm volatile("ld.global.f32 %0, [%1];" : "=f"(old) : "l"(acc + pos));
-                mbar_wait(&full[it & 1], (it >> 1) & 1, dead);
-                float s[G][2][4];
-                q4_scores<G>(sbase + C::kOffQ,
-                             sbase + C::kOffStage + (it & 1) * C::kStageBytes + 16 * warp * kQ4RowBytes, lane, s);
-                __syncthreads();  // every warp is done with the tile
-                if (tid == 0 && t + 2 < tiles) issue(it + 2, tile0 + t + 2);
-                if (!mapped) {
-                    if (g0 == 0 && lane < min(len - pos0, 16)) count_bad_index();
-                    continue;
+            float w[4] = {0.f, 0.f, 0.f, 0.f};  // column 2 c + e of n8 tile i at [2 i + e]
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 l2 = lse_s[8 * h + r];
+                const int lim = lim_s[8 * h + r] - pos0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = fmaf(s[k >> 1][2 * h + (k & 1)], p.scale_log2, -l2.x) - l2.y;
+                    w[k] += 8 * (k >> 1) + q4_row_of(2 * c + (k & 1)) < lim ? fast_exp2(x) : 0.f;
                 }
-                float w[4] = {0.f, 0.f, 0.f, 0.f};  // column 2 c + e of n8 tile i at [2 i + e]
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 l2 = lse_s[16 * g + 8 * h + r];
-                        const int lim = lim_s[16 * g + 8 * h + r] - pos0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = fmaf(s[g][k >> 1][2 * h + (k & 1)], p.scale_log2, -l2.x) - l2.y;
-                            w[k] += 8 * (k >> 1) + q4_row_of(2 * c + (k & 1)) < lim ? fast_exp2(x) : 0.f;
-                        }
-                    }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] += __shfl_xor_sync(0xffffffffu, w[k], o);
-                const float v = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
-                if (mine) acc[pos] = old + v;
             }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] += __shfl_xor_sync(0xffffffffu, w[k], o);
+            const float v = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
+            if (mine) acc[pos] = old + v;
         }
     }
 }
 
-// ---------------------------------------------------------------- bf16 rows
+// ---------------------------------------------------------------- bf16 rows, or more query rows
 // 1152 bytes a row leave the tensor core about 50 cycles per row and SM, so the
 // rows go through tcgen05 with up to 128 query rows at once, the indexer's way:
-// the CACHE ROWS are M = 128 (two pages, each a column of TMA boxes of 64 rows x
-// 64 values, 128B swizzle), the query rows N, and the accumulator holds one
-// position per TMEM lane: the epilogue thread that owns a position adds up its
-// columns alone.  A CTA (one per SM) takes an equal run of the batch's pages.
-// Warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warps 4-7 epilogue.
-struct WeighTcCfg {
-    static constexpr int kThreads = 256;
+// the CACHE ROWS are M = 128 (two pages), the query rows N, and the accumulator
+// holds one position per TMEM lane: the epilogue thread that owns a position adds
+// up its columns alone.  A CTA (one per SM) takes an equal run of the batch's
+// pages.  More query rows than 128 go in further passes over the run.
+//   bf16 rows  boxes of 128 rows x 64 values by TMA (128B swizzle), A in shared
+//              memory.
+//   4-bit rows pages by bulk copies; the lane that owns a row decodes it into
+//              TMEM, where it is the A operand: no decoded row passes through
+//              shared memory.
+// The MMA issuer takes three boxes of 64 values at a time: a wait, twelve MMAs, a
+// commit.  Each such turn costs some 390 cycles beside its MMAs (about 60 each with
+// A in TMEM), and one per box took 31 us where this takes 22 (4-bit rows, 37
+// sequences of 4096 positions).
+// Warp 0 rows in, warp 1 TMEM owner and MMA issuer, warps 4-7 epilogue; 4-bit
+// rows: warp 2 queries in, warps 8-15 decode.
+// Measured: 72 query rows over 46089 positions, bf16 15.9 us (8.2 us at the
+// memory's rate, 43 us by mma.sync): 2.4 steps of 128 rows a CTA, so launch,
+// queries and the first boxes are half of it; 4-bit 13.5 us (mma.sync in three
+// passes 30.8).  37 sequences of 4096 positions, 4-bit rows: 24 query rows 22.4
+// us, 64 23.9, 72 25.1 (mma.sync with 32, 64, 32 rows a pass: 23.0, 37.2, 63.3).
+template <bool Q4>
+struct WeighCfg {
+    static constexpr int kThreads = Q4 ? 512 : 256;
     static constexpr int kMaxRows = 128;                  // query rows per pass (the MMA's N)
-    static constexpr int kBoxBytes = 2 * 64 * 128;        // 128 cache rows x 64 values
-    static constexpr int kMaxStages = 12;
-    static constexpr int kTmemCols = 2 * kMaxRows;        // two accumulators
-    // full[], empty[], q_full, q_empty, acc_full[2], acc_empty[2]
-    static constexpr int kNumBars = 2 * kMaxStages + 6;
+    // the ring: boxes of 128 cache rows x 64 values, or pages of 4-bit rows
+    static constexpr int kStageBytes = Q4 ? 64 * kQ4RowBytes : 2 * 64 * 128;
+    static constexpr int kMaxStages = Q4 ? 7 : 12;
+    static constexpr int kChunks = 2;                     // Q4: decoded chunks in TMEM, of
+    static constexpr int kChunkBoxes = 3;                 // three boxes (64 values: 32 columns) each
+    static constexpr int kChunkCols = 32 * kChunkBoxes;
+    static constexpr int kTmemCols = Q4 ? 512 : 2 * kMaxRows;  // two accumulators, then the chunks
+    // full[], empty[], q_full, q_empty, acc_full[2], acc_empty[2], chunk_full[], chunk_free[]
+    static constexpr int kNumBars = 2 * kMaxStages + 6 + (Q4 ? 2 * kChunks : 0);
     static constexpr int kOffRow = 0;                     // float4 [kMaxRows]: lse (two parts), visible positions
     static constexpr int kOffBar = kOffRow + 16 * kMaxRows;
     static constexpr int kOffTmem = kOffBar + 8 * kNumBars;
@@ -175,16 +183,18 @@ struct WeighTcCfg {
     static constexpr int kOffQ = (kOffScratch + 192 + 1023) / 1024 * 1024;  // [9][npad rows x 128 B], then the ring
     static constexpr int kSmemBytes = 232448;
     __host__ __device__ static constexpr int stages(int npad) {
-        const int n = (kSmemBytes - 1024 - kOffQ - npad * kRowBytes) / kBoxBytes;
+        const int n = (kSmemBytes - 1024 - kOffQ - npad * kRowBytes) / kStageBytes;
         return n < kMaxStages ? n : kMaxStages;
     }
 };
-static_assert(WeighTcCfg::stages(128) >= 4, "ring of boxes");
+static_assert(WeighCfg<false>::stages(128) >= 4, "ring of boxes");
+static_assert(WeighCfg<true>::stages(128) >= 3, "ring of pages");
 
-__global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
-    smla_weigh_bf16_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
-                           const WeighParams a) {
-    using C = WeighTcCfg;
+template <bool Q4>
+__global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
+    smla_weigh_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
+                      const WeighParams a) {
+    using C = WeighCfg<Q4>;
     const PartialParams &p = a.p;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -195,6 +205,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kMaxStages;
     uint64_t *q_full = empty + C::kMaxStages, *q_empty = q_full + 1;
     uint64_t *acc_full = q_empty + 1, *acc_empty = acc_full + 2;
+    uint64_t *chunk_full = acc_empty + 2, *chunk_free = chunk_full + C::kChunks;  // Q4
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
     const uint32_t sbase = smem_addr(smem);
     const uint32_t q_addr = sbase + C::kOffQ, ring = q_addr + npad * kRowBytes;
@@ -202,13 +213,19 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kMaxStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], Q4 ? 4 : 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 128);
+        }
+        if constexpr (Q4) {
+            for (int i = 0; i < C::kChunks; ++i) {
+                mbar_init(&chunk_full[i], 4);
+                mbar_init(&chunk_free[i], 1);
+            }
         }
         fence_mbar_init();
     }
@@ -218,8 +235,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
-    const Q4Run run = q4_find_run<64>(p, a.grid, 2, nullptr,
-                                      reinterpret_cast<int *>(smem + C::kOffScratch));
+    const Q4Run run = q4_find_run<64>(p, a.grid, 2, nullptr, reinterpret_cast<int *>(smem + C::kOffScratch));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -229,7 +245,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
     // (of kMaxRows query rows) and steps (of two pages).
     auto walk = [&](auto &&body) {
         int b = run.b, page0 = run.tile;
-        for (long long at = run.begin; at < run.end; ++b, page0 = 0) {
+        for (long long at = run.begin; at < run.end && !dead; ++b, page0 = 0) {
             const int len = at == run.begin ? run.len : q4_seq_len(p, b, false);
             const int pages = (int)min((long long)((len + 63) / 64 - page0), run.end - at);
             if (pages <= 0) continue;
@@ -238,19 +254,36 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
         }
     };
 
+    // a pass's queries: nine boxes of npad rows x 64 values
+    auto load_q = [&](int b, int g0, int &pass) {
+        if (pass > 0) mbar_wait(q_empty, (pass - 1) & 1, dead);
+        ++pass;
+        mbar_arrive_expect_tx(q_full, (uint32_t)(npad * kRowBytes));
+        const uint64_t keep = l2_policy_evict_last();
+#pragma unroll 1
+        for (int k = 0; k < 9; ++k) tma_load_2d(q_addr + k * npad * 128, &map_q, 64 * k, b * rows + g0, q_full, keep);
+    };
+
     if (warp == 0) {
-        // ============================================================ TMA producer
+        // ============================================================ rows in
         if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
-            int st = 0, round = 0, piece = 0;
+            const uint64_t once = l2_policy_evict_first();
+            int st = 0, round = 0, pass = 0;
             walk([&](int b, int len, int page0, int pages, int g0) {
                 const int *pt_b = p.page_table + (size_t)b * p.pt_stride;
-                if (piece > 0) mbar_wait(q_empty, (piece - 1) & 1, dead);
-                ++piece;
-                mbar_arrive_expect_tx(q_full, (uint32_t)(npad * kRowBytes));
-#pragma unroll 1
-                for (int k = 0; k < 9; ++k)
-                    tma_load_2d(q_addr + k * npad * 128, &map_q, 64 * k, b * rows + g0, q_full, keep);
+                if constexpr (Q4) {
+                    for (int t = 0; t < pages && !dead; ++t) {
+                        const int pg = q4_page(pt_b, p.pt_stride, p.num_pages, page0 + t);
+                        if (round > 0) mbar_wait(&empty[st], (round - 1) & 1, dead);
+                        q4_copy_page(p, pg, smem + (ring - sbase) + st * C::kStageBytes, &full[st]);
+                        if (++st == nst) {
+                            st = 0;
+                            ++round;
+                        }
+                    }
+                    return;
+                }
+                load_q(b, g0, pass);
                 for (int t = 0; t < pages; t += 2) {
                     const int pg0 = q4_page(pt_b, p.pt_stride, p.num_pages, page0 + t);
                     const int pg1 = t + 1 < pages ? q4_page(pt_b, p.pt_stride, p.num_pages, page0 + t + 1) : -1;
@@ -259,7 +292,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
                     for (int k = 0; k < 9; ++k) {
                         if (round > 0) mbar_wait(&empty[st], (round - 1) & 1, dead);
                         mbar_arrive_expect_tx(&full[st], bytes);
-                        const uint32_t dst = ring + st * C::kBoxBytes;
+                        const uint32_t dst = ring + st * C::kStageBytes;
                         if (pg0 >= 0) tma_load_2d(dst, &map_kv, 64 * k, pg0 * 64, &full[st], once);
                         if (pg1 >= 0) tma_load_2d(dst + 8192, &map_kv, 64 * k, pg1 * 64, &full[st], once);
                         if (++st == nst) {
@@ -271,32 +304,117 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
             });
         }
         __syncwarp();
+    } else if (Q4 && warp == 2) {
+        // ============================================================ queries in
+        if (lane == 0) {
+            int pass = 0;
+            walk([&](int b, int, int, int, int g0) { load_q(b, g0, pass); });
+        }
+        __syncwarp();
+    } else if (Q4 && warp >= 8) {
+        // ============================================================ codes -> TMEM
+        // Lane = cache row; warps 8, 9 and 12, 13 take a step's first page, the others
+        // its second; warps 8-11 and 12-15 take turns at the chunks.
+        // (A row that nobody sees, or that no page maps, is garbage in its own
+        // lane alone.)
+        const int w = warp & 3, half = w >> 1, turn = (warp - 8) >> 2;
+        int idx = 0, c = 0;  // pages and chunks so far
+        walk([&](int, int, int, int pages, int) {
+            for (int t = 0; t < pages; t += 2) {
+                const int page = idx + t + half, st = page % nst;
+                const bool has = t + half < pages;
+                if (has) mbar_wait(&full[st], (page / nst) & 1, dead);
+                const uint32_t row = ring + st * C::kStageBytes + (32 * (w & 1) + lane) * kQ4RowBytes;
+                uint32_t sc[8];
+                if (has) {
+                    const uint4 x = lds_16(row + kQ4OffScale), y = lds_16(row + kQ4OffScale + 16);
+                    sc[0] = x.x, sc[1] = x.y, sc[2] = x.z, sc[3] = x.w;
+                    sc[4] = y.x, sc[5] = y.y, sc[6] = y.z, sc[7] = y.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 9 / C::kChunkBoxes; ++j, ++c) {
+                    if ((c & 1) != turn) continue;
+                    if (c >= C::kChunks) mbar_wait(&chunk_free[turn], (c / C::kChunks - 1) & 1, dead);
+                    tc_fence_after();
+                    if (has) {
+#pragma unroll
+                        for (int k = C::kChunkBoxes * j; k < C::kChunkBoxes * (j + 1); ++k) {
+                            uint32_t v[32];
+                            if (k < 8) {
+                                const uint4 a0 = lds_16(row + 32 * k), a1 = lds_16(row + 32 * k + 16);
+                                const uint32_t word[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+                                for (int g = 0; g < 8; ++g) {
+                                    const uint32_t s2 = __byte_perm(sc[k & 7], 0u, g < 4 ? 0x1010 : 0x3232);
+                                    const uint4 x = q4_word(word[g], s2, q4_bias(s2));
+                                    v[4 * g] = x.x, v[4 * g + 1] = x.y, v[4 * g + 2] = x.z, v[4 * g + 3] = x.w;
+                                }
+                            } else {
+#pragma unroll
+                                for (int g = 0; g < 8; ++g) {
+                                    const uint4 x = lds_16(row + kQ4OffRope + 16 * g);
+                                    v[4 * g] = x.x, v[4 * g + 1] = x.y, v[4 * g + 2] = x.z, v[4 * g + 3] = x.w;
+                                }
+                            }
+                            tmem_st32(tmem + ((uint32_t)(32 * w) << 16) + 2 * C::kMaxRows + C::kChunkCols * turn +
+                                          32 * (k % C::kChunkBoxes), v);
+                        }
+                        tmem_st_wait();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&chunk_full[turn]);
+                }
+                __syncwarp();
+                if (has && lane == 0) mbar_arrive(&empty[st]);
+            }
+            idx += pages;
+        });
+        tc_fence_before();
     } else if (warp == 1) {
         // ============================================================ MMA issuer
         if (lane == 0) {
             const uint32_t idesc = idesc_bf16_f32(128, npad, false, false);
-            int st = 0, round = 0, piece = 0, step = 0;
+            const int n = Q4 ? C::kChunks : nst;
+            uint64_t *in = Q4 ? chunk_full : full, *out = Q4 ? chunk_free : empty;
+            int st = 0, round = 0, pass = 0, step = 0;
             walk([&](int, int, int, int pages, int) {
-                mbar_wait(q_full, piece & 1, dead);
-                ++piece;
+                mbar_wait(q_full, pass & 1, dead);
+                ++pass;
                 for (int t = 0; t < pages; t += 2, ++step) {
                     const int acc = step & 1;
                     if (step >= 2) mbar_wait(&acc_empty[acc], ((step >> 1) - 1) & 1, dead);
                     tc_fence_after();
+                    const uint32_t d = tmem + acc * C::kMaxRows;
 #pragma unroll 1
-                    for (int k = 0; k < 9; ++k) {
-                        mbar_wait(&full[st], round & 1, dead);
-                        tc_fence_after();
-                        const uint64_t ad = smem_desc(ring + st * C::kBoxBytes, 16, 1024, kSwizzle128B);
-                        const uint64_t bd = smem_desc(q_addr + k * npad * 128, 16, 1024, kSwizzle128B);
+                    for (int k0 = 0; k0 < 9; k0 += C::kChunkBoxes) {
+                        int box_st[C::kChunkBoxes];  // bf16: where the boxes are
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + acc * C::kMaxRows, ad + 2 * kk, bd + 2 * kk, idesc, (k | kk) ? 1u : 0u);
-                        umma_commit(&empty[st]);
-                        if (++st == nst) {
-                            st = 0;
-                            ++round;
+                        for (int k = 0; k < (Q4 ? 1 : C::kChunkBoxes); ++k) {
+                            mbar_wait(&in[st], round & 1, dead);
+                            box_st[k] = st;
+                            if (++st == n) {
+                                st = 0;
+                                ++round;
+                            }
                         }
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < C::kChunkBoxes; ++k) {
+                            const uint64_t bd = smem_desc(q_addr + (k0 + k) * npad * 128, 16, 1024, kSwizzle128B);
+                            const uint64_t ad = Q4 ? 0 : smem_desc(ring + box_st[k] * C::kStageBytes, 16, 1024, kSwizzle128B);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint32_t add = (k0 | k | kk) ? 1u : 0u;
+                                if constexpr (Q4)
+                                    umma_bf16_ts(d, tmem + 2 * C::kMaxRows + C::kChunkCols * box_st[0] + 32 * k + 8 * kk, bd + 2 * kk,
+                                                 idesc, add);
+                                else
+                                    umma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, add);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < (Q4 ? 1 : C::kChunkBoxes); ++k) umma_commit(&out[box_st[k]]);
                     }
                     umma_commit(&acc_full[acc]);
                 }
@@ -304,7 +422,7 @@ __global__ void __launch_bounds__(WeighTcCfg::kThreads, 1)
             });
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ============================================================ epilogue
         const int row = threadIdx.x - 128;  // TMEM lane: cache row of the step's two pages
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
