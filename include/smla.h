@@ -40,7 +40,8 @@
  * Common rules for every entry point:
  *  - All pointers are DEVICE pointers on the current device, owned by the
  *    caller, except the per-step buffers of smla_decode_host (pinned host
- *    memory).  The library allocates no device memory at run time; it keeps a
+ *    memory) and the two short arrays of smla_evict_apply (host memory, read
+ *    during the call).  The library allocates no device memory at run time; it keeps a
  *    small host-side cache of per-device kernel attributes and, for
  *    smla_decode_noalloc, one static device array per GPU.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL is
