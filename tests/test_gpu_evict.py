@@ -83,6 +83,14 @@ def test_weights_over_lengths(lens, q4):
 
 
 @pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("H", [4, 24])
+def test_weights_over_many_ragged_sequences(H, q4):
+    """More sequences than a block has threads, runs that cross many of them, empty ones between."""
+    rng = np.random.default_rng(H)
+    run_weigh([[int(x)] for x in rng.integers(0, 200, 600) * (rng.random(600) < 0.7)], H, q4, seed=H)
+
+
+@pytest.mark.parametrize("q4", [False, True])
 def test_weights_of_rows_with_empty_and_infinite_lse(q4):
     def edit(lse):
         lse[0, 0, 3] = -INF

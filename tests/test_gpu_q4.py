@@ -408,6 +408,18 @@ def test_dense_lengths(lens, H, nsplit):
     run_dense(lens, H, nsplit, seed=len(lens))
 
 
+@pytest.mark.parametrize("H", [3, 40])
+def test_dense_many_ragged_sequences(H):
+    """More sequences than a block has threads, runs that cross many of them, empty ones between."""
+    rng = np.random.default_rng(H)
+    run_dense([[int(x)] for x in rng.integers(0, 200, 300) * (rng.random(300) < 0.7)], H, 0, seed=H)
+
+
+def test_dense_one_long_sequence_among_many_empty():
+    """Its pieces outnumber the combine's threads."""
+    run_dense([[0]] * 400 + [[39000]] + [[1]] * 199, 2, 0, seed=1)
+
+
 def test_dense_bound_above_every_length():
     run_dense([[70], [300]], 16, 0, K=4096)
     run_dense([[70], [300]], 64, 0, K=4096)
