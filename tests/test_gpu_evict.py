@@ -98,13 +98,14 @@ def test_weights_of_rows_with_empty_and_infinite_lse(q4):
     run_weigh([[90, 100]], 8, q4, lse_edit=edit)
 
 
+@pytest.mark.parametrize("H", [4, 16])
 @pytest.mark.parametrize("q4", [False, True])
-def test_weights_ignore_what_lies_behind_the_length(q4):
+def test_weights_ignore_what_lies_behind_the_length(q4, H):
     """NaN rows in the masked part of a page and of the pool change nothing."""
     paged = cu.Paged([40], 1)
     cache, vals = make_cache(paged, q4, 2)
-    q, lens = cu.queries(1, 2, 16, 3), torch.tensor([[30, 37]], dtype=torch.int32).cuda()
-    lse = torch.zeros(1, 2, 16).cuda() + 4.0
+    q, lens = cu.queries(1, 2, H, 3), torch.tensor([[30, 37]], dtype=torch.int32).cuda()
+    lse = torch.zeros(1, 2, H).cuda() + 4.0
     acc = torch.zeros(1, 40).cuda()
     binding.evict_accumulate(q.cuda(), cache, paged.cuda, lens, lse, SCALE, acc)
     flat = cache.view(-1, cache.shape[-1])
@@ -116,11 +117,27 @@ def test_weights_ignore_what_lies_behind_the_length(q4):
     assert torch.equal(acc, acc2) and not acc[0, 37:].any()
 
 
-def test_weights_count_bad_lengths_and_pages():
+@pytest.mark.parametrize("H", [4, 20])
+@pytest.mark.parametrize("q4", [False, True])
+def test_weights_of_a_sequence_ignore_its_neighbours_queries(q4, H):
+    """NaN queries and statistics of one sequence stay out of the other's weights."""
+    paged = cu.Paged([70, 70], 1)
+    cache, vals = make_cache(paged, q4, 2)
+    q, lse = cu.queries(2, 1, H, 3).cuda(), torch.zeros(2, 1, H).cuda() + 4.0
+    lens = torch.tensor([[70], [70]], dtype=torch.int32).cuda()
+    want = binding.evict_accumulate(q, cache, paged.cuda, lens, lse, SCALE, torch.zeros(2, 70).cuda())
+    q[1], lse[1] = float("nan"), float("nan")
+    got = binding.evict_accumulate(q, cache, paged.cuda, lens, lse, SCALE, torch.zeros(2, 70).cuda())
+    assert torch.equal(got[0], want[0]) and got[1].isnan().all()
+
+
+@pytest.mark.parametrize("H", [4, 20])
+@pytest.mark.parametrize("q4", [False, True])
+def test_weights_count_bad_lengths_and_pages(q4, H):
     paged = cu.Paged([128, 128], 1)
     paged.table[0, 1] = 10 ** 6
-    cache, vals = make_cache(paged, False, 2)
-    q, lse = cu.queries(2, 1, 4, 3).cuda(), torch.zeros(2, 1, 4).cuda()
+    cache, vals = make_cache(paged, q4, 2)
+    q, lse = cu.queries(2, 1, H, 3).cuda(), torch.zeros(2, 1, H).cuda()
     acc = torch.zeros(2, 100).cuda()
     lens = torch.tensor([[100], [-3]], dtype=torch.int32).cuda()
     binding.evict_accumulate(q, cache, paged.cuda, lens, lse, SCALE, acc)
