@@ -1509,7 +1509,8 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
 }
 
 // CTAs per sequence of the plan: as many as keep the whole batch in one wave,
-// while each still has a thread per slot.
+// while each still has a thread per slot.  (With 1, 2, 4, 8: 2048 slots 13.4, 12.7,
+// 13.1, 14.4 us; 8448 slots 23.9, 18.7, 16.2, 16.1; 32768 slots 53.5, 33.6, 23.8, 19.8.)
 int plan_cluster(int B, int max_n, int sms) {
     int nc = 1;
     while (nc < smla::kPlanMaxCluster && 2ll * nc * B <= sms && 2ll * nc * smla::kPlanThreads <= max_n) nc *= 2;
