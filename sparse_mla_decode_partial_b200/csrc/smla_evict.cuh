@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(32) smla_evict_apply_bulk_kernel(const EvictAp
                     off += bytes;
                 }
             mbar_wait(&bar, phase, dead);
+            dead = __any_sync(0xffffffffu, dead);  // the warp stays together
             phase ^= 1u;
             if (mine && !dead) {
                 for (int k = 0, off = 0; k < p.n_buf; ++k) {

@@ -492,7 +492,9 @@ __host__ __device__ __forceinline__ int q4_sharers(int grid, int min_tiles, long
 }
 
 // A CTA's run [begin, end) of the flattened tiles of TILE positions: total
-// first, then the sequence (b, of length len) and the tile it starts in.  Every thread calls it;
+// first, then the sequence (b, of length len) and the tile it starts in.  Who
+// walks the run stops at the last sequence too: lengths that someone writes
+// during the launch must not send it on for ever.  Every thread calls it;
 // scratch holds 48 ints of shared memory.  The first CTA counts bad lengths.
 struct Q4Run {
     long long total, begin, end;
@@ -518,6 +520,7 @@ __device__ __forceinline__ Q4Run q4_find_run(const PartialParams &p, int grid, i
     r.begin = r.total * blockIdx.x / sharers;
     r.end = r.total * (blockIdx.x + 1) / sharers;
     long long before = 0;
+    if (p.B > (int)blockDim.x && threadIdx.x == 0) scratch[40] = p.B;  // (none, should the lengths change meanwhile)
     for (int b0 = 0; b0 < p.B && before <= r.begin; b0 += blockDim.x) {
         const int b = b0 + threadIdx.x;
         if (p.B > (int)blockDim.x) {  // else the counts above are still those of this chunk
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     Q4Consumer w;
     w.init(warp, lane);
     int it = 0;
-    for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
+    for (long long at = run.begin; at < run.end && b < p.B; ++b, tile0 = 0) {
         const int len = q4_seq_len(p, b, false);  // (run.len in a register through the loop: 110.6 us where this takes 108.4)
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;  // a sequence that sees nothing

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(WeighQ4Cfg::kThreads, WeighQ4Cfg::kMinBlocks)
                                             reinterpret_cast<int *>(smem + C::kOffScratch));
     const int rows = p.dense_t * p.dense_h;
     int b = run.b, tile0 = run.tile, it = 0;
-    for (long long at = run.begin; at < run.end; ++b, tile0 = 0) {
+    for (long long at = run.begin; at < run.end && b < p.B; ++b, tile0 = 0) {
         const int len = at == run.begin ? run.len : q4_seq_len(p, b, false);
         const int tiles = (int)min((long long)((len + C::kTile - 1) / C::kTile - tile0), run.end - at);
         if (tiles <= 0) continue;
@@ -173,7 +173,16 @@ struct WeighCfg {
     static constexpr int kChunks = 2;                     // Q4: decoded chunks in TMEM, of
     static constexpr int kChunkBoxes = 3;                 // three boxes (64 values: 32 columns) each
     static constexpr int kChunkCols = 32 * kChunkBoxes;
-    static constexpr int kTmemCols = Q4 ? 512 : 2 * kMaxRows;  // two accumulators, then the chunks
+    // A score is added up in parts, of every second or third chunk each, which the
+    // epilogue adds: the tensor core cuts partial sums towards zero, and 36 cuts in
+    // one chain left weights 1.7e-6 off (bf16 rows; 0.5e-6 in three parts, where
+    // plain fp32 sums are 0.2e-6 off; 4-bit rows 0.7e-6 in one, 0.4e-6 in two).  A
+    // part is npad columns; steps alternate between two sets of parts where they fit.
+    static constexpr int kTmemCols = 512;
+    static constexpr int kChunkCol = kTmemCols - (Q4 ? kChunks * kChunkCols : 0);
+    static constexpr int kMaxParts = Q4 ? 2 : 3;
+    __host__ __device__ static constexpr int parts(int npad) { return 2 * kMaxParts * npad <= kChunkCol ? kMaxParts : 2; }
+    __host__ __device__ static constexpr int sets(int npad) { return 2 * parts(npad) * npad <= kChunkCol ? 2 : 1; }
     // full[], empty[], q_full, q_empty, acc_full[2], acc_empty[2], chunk_full[], chunk_free[]
     static constexpr int kNumBars = 2 * kMaxStages + 6 + (Q4 ? 2 * kChunks : 0);
     static constexpr int kOffRow = 0;                     // float4 [kMaxRows]: lse (two parts), visible positions
@@ -189,6 +198,8 @@ struct WeighCfg {
 };
 static_assert(WeighCfg<false>::stages(128) >= 4, "ring of boxes");
 static_assert(WeighCfg<true>::stages(128) >= 3, "ring of pages");
+static_assert(WeighCfg<false>::sets(128) == 2 && WeighCfg<true>::parts(128) * 128 <= WeighCfg<true>::kChunkCol,
+              "parts of a score");
 
 template <bool Q4>
 __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.dense_t * p.dense_h;
     const int npad = min((rows + 15) / 16 * 16, C::kMaxRows);
-    const int nst = C::stages(npad);
+    const int nst = C::stages(npad), nset = C::sets(npad), parts = C::parts(npad);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::kMaxStages;
     uint64_t *q_full = empty + C::kMaxStages, *q_empty = q_full + 1;
     uint64_t *acc_full = q_empty + 1, *acc_empty = acc_full + 2;
@@ -241,11 +252,13 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
+    // (A thread whose wait gave up goes on without waiting: one that left would
+    // keep the others at their barriers.)
     // Every role walks the same pieces (a run of one sequence's pages), passes
     // (of kMaxRows query rows) and steps (of two pages).
     auto walk = [&](auto &&body) {
         int b = run.b, page0 = run.tile;
-        for (long long at = run.begin; at < run.end && !dead; ++b, page0 = 0) {
+        for (long long at = run.begin; at < run.end && b < p.B; ++b, page0 = 0) {
             const int len = at == run.begin ? run.len : q4_seq_len(p, b, false);
             const int pages = (int)min((long long)((len + 63) / 64 - page0), run.end - at);
             if (pages <= 0) continue;
@@ -356,7 +369,7 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
                                     v[4 * g] = x.x, v[4 * g + 1] = x.y, v[4 * g + 2] = x.z, v[4 * g + 3] = x.w;
                                 }
                             }
-                            tmem_st32(tmem + ((uint32_t)(32 * w) << 16) + 2 * C::kMaxRows + C::kChunkCols * turn +
+                            tmem_st32(tmem + ((uint32_t)(32 * w) << 16) + C::kChunkCol + C::kChunkCols * turn +
                                           32 * (k % C::kChunkBoxes), v);
                         }
                         tmem_st_wait();
@@ -382,10 +395,9 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
                 mbar_wait(q_full, pass & 1, dead);
                 ++pass;
                 for (int t = 0; t < pages; t += 2, ++step) {
-                    const int acc = step & 1;
-                    if (step >= 2) mbar_wait(&acc_empty[acc], ((step >> 1) - 1) & 1, dead);
+                    const int acc = step % nset;
+                    if (step >= nset) mbar_wait(&acc_empty[acc], (step / nset - 1) & 1, dead);
                     tc_fence_after();
-                    const uint32_t d = tmem + acc * C::kMaxRows;
 #pragma unroll 1
                     for (int k0 = 0; k0 < 9; k0 += C::kChunkBoxes) {
                         int box_st[C::kChunkBoxes];  // bf16: where the boxes are
@@ -399,15 +411,17 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
                             }
                         }
                         tc_fence_after();
+                        const uint32_t d = tmem + (acc * parts + k0 / C::kChunkBoxes % parts) * npad;
+                        const bool first = k0 < parts * C::kChunkBoxes;
 #pragma unroll
                         for (int k = 0; k < C::kChunkBoxes; ++k) {
                             const uint64_t bd = smem_desc(q_addr + (k0 + k) * npad * 128, 16, 1024, kSwizzle128B);
                             const uint64_t ad = Q4 ? 0 : smem_desc(ring + box_st[k] * C::kStageBytes, 16, 1024, kSwizzle128B);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                const uint32_t add = (k0 | k | kk) ? 1u : 0u;
+                                const uint32_t add = first && (k | kk) == 0 ? 0u : 1u;
                                 if constexpr (Q4)
-                                    umma_bf16_ts(d, tmem + 2 * C::kMaxRows + C::kChunkCols * box_st[0] + 32 * k + 8 * kk, bd + 2 * kk,
+                                    umma_bf16_ts(d, tmem + C::kChunkCol + C::kChunkCols * box_st[0] + 32 * k + 8 * kk, bd + 2 * kk,
                                                  idesc, add);
                                 else
                                     umma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, add);
@@ -444,26 +458,30 @@ __global__ void __launch_bounds__(WeighCfg<Q4>::kThreads, 1)
                 const bool mine = page < page0 + pages && pos < len;
                 const bool mapped = mine && q4_page(pt_b, p.pt_stride, p.num_pages, page) >= 0;
                 if (mine && !mapped && g0 == 0) count_bad_index();
-                float sum = 0.f;
-                if (mapped) asm volatile("ld.global.f32 %0, [%1];" : "=f"(sum) : "l"(acc_b + pos));
-                mbar_wait(&acc_full[step & 1], (step >> 1) & 1, dead);
+                float old = 0.f;
+                if (mapped) asm volatile("ld.global.f32 %0, [%1];" : "=f"(old) : "l"(acc_b + pos));
+                mbar_wait(&acc_full[step % nset], (step / nset) & 1, dead);
                 tc_fence_after();
                 float w = 0.f;
 #pragma unroll 1
                 for (int n = 0; n < npad; n += 16) {
-                    uint32_t s[16];
-                    tmem_ld_cols<16>(t_lane + (step & 1) * C::kMaxRows + n, s);
+                    uint32_t s[C::kMaxParts][16];
+#pragma unroll
+                    for (int j = 0; j < C::kMaxParts; ++j)  // (a third part that is none: the second again)
+                        tmem_ld_cols<16>(t_lane + (step % nset * parts + min(j, parts - 1)) * npad + n, s[j]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float4 q = row_s[n + k];
-                        const float x = fmaf(__uint_as_float(s[k]), p.scale_log2, -q.x) - q.y;
+                        float sum = __uint_as_float(s[0][k]) + __uint_as_float(s[1][k]);
+                        if (C::kMaxParts == 3) sum = parts == 3 ? sum + __uint_as_float(s[C::kMaxParts - 1][k]) : sum;
+                        const float x = fmaf(sum, p.scale_log2, -q.x) - q.y;
                         w += pos < __float_as_int(q.z) ? fast_exp2(x) : 0.f;
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&acc_empty[step & 1]);
-                if (mapped) acc_b[pos] = sum + w;
+                mbar_arrive(&acc_empty[step % nset]);
+                if (mapped) acc_b[pos] = old + w;
             }
         });
         tc_fence_before();
