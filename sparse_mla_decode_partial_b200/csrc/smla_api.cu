@@ -1503,7 +1503,7 @@ smla_status evict_accumulate(const void *q, const void *cache, int64_t num_pages
     a.lse = lse;
     a.acc = acc;
     // (Measured, 37 sequences of 4096 positions, the small kernel and the other:
-    // 16 query rows 18.6 and 22.0 us, 24 rows, in two passes, 32 and 22.5.)
+    // 16 query rows 18.5 and 23 us, 24 rows, in two passes, 32 and 23.4.)
     if (Q4 && rows <= kQ4Rows) return launch_weigh_q4(a, st);
     return launch_weigh<Q4>(a, st);
 }

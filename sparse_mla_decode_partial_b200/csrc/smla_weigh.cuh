@@ -154,15 +154,17 @@ __global__ void __launch_bounds__(WeighQ4Cfg::kThreads, WeighQ4Cfg::kMinBlocks)
 //              shared memory.
 // The MMA issuer takes three boxes of 64 values at a time: a wait, twelve MMAs, a
 // commit.  Each such turn costs some 390 cycles beside its MMAs (about 60 each with
-// A in TMEM), and one per box took 31 us where this takes 22 (4-bit rows, 37
+// A in TMEM), and one per box took 31 us where this took 22 (4-bit rows, 37
 // sequences of 4096 positions).
 // Warp 0 rows in, warp 1 TMEM owner and MMA issuer, warps 4-7 epilogue; 4-bit
 // rows: warp 2 queries in, warps 8-15 decode.
-// Measured: 72 query rows over 46089 positions, bf16 15.9 us (8.2 us at the
+// Measured: 72 query rows over 46089 positions, bf16 16.8 us (8.2 us at the
 // memory's rate, 43 us by mma.sync): 2.4 steps of 128 rows a CTA, so launch,
-// queries and the first boxes are half of it; 4-bit 13.5 us (mma.sync in three
-// passes 30.8).  37 sequences of 4096 positions, 4-bit rows: 24 query rows 22.4
-// us, 64 23.9, 72 25.1 (mma.sync with 32, 64, 32 rows a pass: 23.0, 37.2, 63.3).
+// queries and the first boxes are half of it; 4-bit 13.8 us (mma.sync in three
+// passes 30.8).  37 sequences of 4096 positions, 4-bit rows: 24 query rows 23.4
+// us, 64 24.7, 72 26.2 (mma.sync with 32, 64, 32 rows a pass: 23.0, 37.2, 63.3);
+// bf16 rows: 16 to 64 query rows 30 us, 96 33.5 (27 us at the memory's rate), 128
+// 50, where the queries leave the ring four boxes.
 template <bool Q4>
 struct WeighCfg {
     static constexpr int kThreads = Q4 ? 512 : 256;
