@@ -217,6 +217,19 @@ def test_sparse_widths(K, H, nsplit):
     run_sparse([600], 1, H, lists_for([600], 1, K, K), nsplit, seed=K + 1)
 
 
+@pytest.mark.parametrize("H", [3, 16, 40])
+def test_one_row_comes_out_as_it_is(H):
+    """A softmax over one row is 1: o is the row's latents, bit for bit."""
+    paged = cu.Paged([90, 70], 1)
+    cache, vals = fill(paged, [90, 70], 2)
+    q, idx = cu.queries(2, 1, H, 3).cuda(), torch.tensor([[[77]], [[3]]], dtype=torch.int32).cuda()
+    want = binding.q4_read(cache, paged.cuda, idx[:, 0])[:, :, None, :512].expand(2, 1, H, 512)
+    assert torch.equal(binding.decode_q4(q, cache, paged.cuda, idx, SCALE)[0], want)
+    first = binding.q4_read(cache, paged.cuda, torch.zeros_like(idx[:, 0]))[:, :, None, :512].expand(2, 1, H, 512)
+    one = torch.ones(2, 1, dtype=torch.int32).cuda()
+    assert torch.equal(binding.decode_dense_q4(q, cache, paged.cuda, one, SCALE, K=1)[0], first)
+
+
 @pytest.mark.parametrize("H", [8, 16, 48])
 def test_sparse_long_lists_cross_resolve_chunks(H):
     run_sparse([5000, 4999], 1, H, lists_for([5000, 4999], 1, 4600, 3), 1, seed=5)
