@@ -22,11 +22,12 @@
 // warp reads all four fragments and accumulates its 128 output columns.
 // Running maxima: each warp keeps one per query row over its own rows, rounded
 // up to an integer (log2 units), so that bringing its P to the common maximum
-// is a multiplication by a power of two, exact in bf16: P is rounded once.  (At
-// most 16 rows have one warp and keep their maximum itself, so that a row which
-// is alone has P = 1 and comes out as it is.  Dividing by the sum of the rounded P
-// would give that to any row that dominates, and o 1.93e-3 off in place of 2.0e-3,
-// but took 112.5 us where this takes 108.5.)
+// is a multiplication by a power of two, exact in bf16: P is rounded once.
+// SHORT (at most kQ4Short rows): the output is divided by the sum of the rounded P
+// (lse is that of the others), so that a row which dominates is not off by its P's
+// rounding.  One row comes out bit for bit; 64 rows are off by 2.2e-3 of o in place
+// of 2.5e-3 (its own rounding is 1.7e-3), 2048 by 1.93e-3 in place of 1.95e-3.  It
+// costs 3.5%: 32 sequences as below took 112.5 us.
 // Rows 416 bytes apart: the lane-to-row map below keeps every shared load free
 // of bank conflicts without padding, so a page of the cache lands by one bulk
 // copy.
@@ -49,6 +50,8 @@
 #include "smla_tc_ptx.cuh"
 
 namespace smla {
+
+constexpr int kQ4Short = 512;
 
 struct Q4Cfg {
     static constexpr int kThreads = 128;
@@ -193,11 +196,14 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
 }
 
 // One warp's share of a CTA: scores of 16 rows, 128 output columns.
+template <bool SHORT>
 struct Q4Consumer {
     int warp, lane, r, c;
     float oacc[16][4];
     float mw0, mw1;    // running max (an integer or -inf) of query rows r, r + 8 over this warp's cache rows
     float l0, l1;      // this lane's part of sum exp2(s - mw)
+    uint32_t own[4];   // SHORT: this warp's P, relative to mw, and
+    float racc[4];     // sums of it over the tiles, relative to M (rows r, r, r + 8, r + 8)
     float M0, M1;      // the CTA's running max, what oacc is relative to
 
     __device__ __forceinline__ void init(int warp_, int lane_) {
@@ -210,21 +216,21 @@ struct Q4Consumer {
     __device__ __forceinline__ void reset() {
         mw0 = mw1 = M0 = M1 = -INFINITY;
         l0 = l1 = 0.f;
+        if (SHORT) racc[0] = racc[1] = racc[2] = racc[3] = 0.f;
 #pragma unroll
         for (int n = 0; n < 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
     }
 
     // Masked scores (log2 units, -inf where masked) -> P in this warp's rows'
-    // rope bytes: its A fragment, and the maxima it is relative to.  alone: no
-    // other warp has rows.
-    __device__ __forceinline__ void softmax(uint32_t tile, float (&s)[2][4], bool alone) {
+    // rope bytes: its A fragment, and the maxima it is relative to.
+    __device__ __forceinline__ void softmax(uint32_t tile, float (&s)[2][4]) {
         float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
         float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-        const float n0 = fmaxf(mw0, alone ? x0 : ceilf(x0)), n1 = fmaxf(mw1, alone ? x1 : ceilf(x1));
+        const float n0 = fmaxf(mw0, ceilf(x0)), n1 = fmaxf(mw1, ceilf(x1));
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
         l0 *= fast_exp2(mw0 - u0);  // 2^-inf = 0 before the first visible row
         l1 *= fast_exp2(mw1 - u1);
@@ -239,6 +245,10 @@ struct Q4Consumer {
             l1 += p10 + p11;
             a[2 * i] = pack_bf16x2(p00, p01);
             a[2 * i + 1] = pack_bf16x2(p10, p11);
+        }
+        if (SHORT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) own[i] = a[i];
         }
         __syncwarp();  // every lane has read the rope bytes
         const uint32_t mine = tile + 16 * warp * kQ4RowBytes + kQ4OffRope;
@@ -270,8 +280,17 @@ struct Q4Consumer {
                 oacc[n][2] *= a1;
                 oacc[n][3] *= a1;
             }
+            if (SHORT) {
+                racc[0] *= a0;
+                racc[2] *= a1;
+            }
             M0 = n0;
             M1 = n1;
+        }
+        if (SHORT) {  // a product with ones adds this warp's rounded P up
+            const uint32_t f0 = bf16x2_pow2(mw0 - M0), f1 = bf16x2_pow2(mw1 - M1);
+            mma_bf16_16816(racc, bf16x2_mul(own[0], f0), bf16x2_mul(own[1], f1), bf16x2_mul(own[2], f0),
+                           bf16x2_mul(own[3], f1), 0x3F803F80u, 0x3F803F80u);
         }
         const int ra = q4_row_of(2 * c), rb = q4_row_of(2 * c + 1);
 #pragma unroll
@@ -307,8 +326,9 @@ struct Q4Consumer {
     }
 
     // Total weight of query rows r, r + 8 relative to M, the same in every lane
-    // of a row.  scratch: float2 [4][16] in shared memory; the CTA synchronises.
-    __device__ __forceinline__ void totals(float2 *scratch, float &t0, float &t1) {
+    // of a row, and (SHORT) that of the rounded P.  scratch: float2 [2][4][16] in
+    // shared memory; the CTA synchronises.
+    __device__ __forceinline__ void totals(float2 *scratch, float &t0, float &t1, float &u0, float &u1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -316,9 +336,10 @@ struct Q4Consumer {
         if (c == 0) {
             scratch[16 * warp + r] = make_float2(mw0, l0);
             scratch[16 * warp + r + 8] = make_float2(mw1, l1);
+            if (SHORT) scratch[64 + 16 * warp + r] = make_float2(racc[0], racc[2]);
         }
         __syncthreads();
-        t0 = t1 = 0.f;
+        t0 = t1 = u0 = u1 = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const float2 x = scratch[16 * w + r], y = scratch[16 * w + r + 8];
@@ -326,6 +347,11 @@ struct Q4Consumer {
             // keeps its NaN
             t0 += x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - M0);
             t1 += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M1);
+            if (SHORT) {
+                const float2 z = scratch[64 + 16 * w + r];
+                u0 += z.x;
+                u1 += z.y;
+            }
         }
     }
 };
@@ -356,7 +382,7 @@ __device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q,
 // list starts its pipeline anew.  A cluster of four splits that merge in
 // distributed shared memory took 35.8, but of two 60.8 against 43.7 and of sixteen
 // (15 lists) 23.5 against 14.9.
-template <bool DIRECT>
+template <bool DIRECT, bool SHORT>
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sparse_kernel(const PartialParams p) {
     using C = Q4Cfg;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -394,7 +420,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
                      : "memory");
     };
 
-    Q4Consumer w;
+    Q4Consumer<SHORT> w;
     w.init(warp, lane);
     bool staged = false;
     int it = 0;  // tiles so far: ring position
@@ -425,7 +451,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
                     sc[i][2 + e] = on ? sc[i][2 + e] * p.scale_log2 : -INFINITY;
                 }
             }
-            w.softmax(tile, sc, p.K <= 16);
+            w.softmax(tile, sc);
             __syncthreads();  // P complete; every warp is done with the previous tile
             if (t >= 1 && t - 1 + C::kStages < tiles) issue(it - 1 + C::kStages, t - 1 + C::kStages, n);
             w.output(tile);
@@ -433,8 +459,8 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    float t0, t1;
-    w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1);
+    float t0, t1, u0, u1;
+    w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1, u0, u1);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int h = w.r + 8 * half;
@@ -442,7 +468,8 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
         const float tot = half ? t1 : t0, M = half ? w.M1 : w.M0;
         const bool some = !(tot == 0.f);  // NaN counts
         const size_t row = (size_t)bt * p.H + h;
-        const float inv = !DIRECT ? 1.f : some ? 1.f / tot : 0.f;
+        const float sum = SHORT ? (half ? u1 : u0) : tot;  // what the output is divided by
+        const float inv = DIRECT ? (some ? 1.f / sum : 0.f) : SHORT ? (some ? tot / sum : 1.f) : 1.f;
         // n8 tile n of the accumulators is column 128 warp + 16 (2 c + e) + n
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -460,8 +487,8 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
 #pragma unroll
                 for (int n = 0; n < 16; n += 4)
                     *reinterpret_cast<float4 *>(p.part_o + (row * p.nsplit + s) * kDc + col + n) =
-                        make_float4(w.oacc[n][2 * half + e], w.oacc[n + 1][2 * half + e], w.oacc[n + 2][2 * half + e],
-                                    w.oacc[n + 3][2 * half + e]);
+                        make_float4(w.oacc[n][2 * half + e] * inv, w.oacc[n + 1][2 * half + e] * inv,
+                                    w.oacc[n + 2][2 * half + e] * inv, w.oacc[n + 3][2 * half + e] * inv);
             }
         }
         if (warp == 0 && w.c == 0) {
@@ -567,6 +594,7 @@ __device__ __forceinline__ void q4_copy_page(const PartialParams &p, int pg, uin
              (uint32_t)Q4Cfg::kStageBytes, bar);
 }
 
+template <bool SHORT>
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_dense_kernel(const Q4Params a) {
     using C = Q4Cfg;
     const PartialParams &p = a.p;
@@ -586,7 +614,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     const Q4Run run = q4_find_run<C::kTile>(p, a.grid, 1, a.prefix, scratch);
     const int nrows = p.dense_t * p.dense_h;
     int b = run.b, tile0 = run.tile;
-    Q4Consumer w;
+    Q4Consumer<SHORT> w;
     w.init(warp, lane);
     int it = 0;
     for (long long at = run.begin; at < run.end && b < p.B; ++b, tile0 = 0) {
@@ -644,7 +672,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
                     sc[i][2 + e] = pos < lim1 ? sc[i][2 + e] * p.scale_log2 : -INFINITY;
                 }
             }
-            w.softmax(tile, sc, p.K <= 16);
+            w.softmax(tile, sc);
             fence_proxy_async_smem();  // P and cleared scales, before a later bulk copy writes there
             __syncthreads();  // P complete; every warp is done with the previous tile
             if (tid == 0 && t >= 1 && t - 1 + C::kStages < tiles) issue(it - 1 + C::kStages, next);
@@ -652,24 +680,26 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
         }
         // ---- the piece
         __syncthreads();
-        float t0, t1;
-        w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1);
+        float t0, t1, u0, u1;
+        w.totals(reinterpret_cast<float2 *>(smem + C::kOffStage), t0, t1, u0, u1);
         const size_t slot = (size_t)blockIdx.x + b;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int h = w.r + 8 * half;
             if (h >= nrows) continue;
+            const float tot = half ? t1 : t0;
+            const bool some = !(tot == 0.f);
+            const float inv = SHORT ? (some ? tot / (half ? u1 : u0) : 1.f) : 1.f;
             float *dst = a.piece_o + (slot * C::kRows + h) * kDc + 128 * warp + 32 * w.c;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int n = 0; n < 16; n += 4)
                     *reinterpret_cast<float4 *>(dst + 16 * e + n) =
-                        make_float4(w.oacc[n][2 * half + e], w.oacc[n + 1][2 * half + e], w.oacc[n + 2][2 * half + e],
-                                    w.oacc[n + 3][2 * half + e]);
+                        make_float4(w.oacc[n][2 * half + e] * inv, w.oacc[n + 1][2 * half + e] * inv,
+                                    w.oacc[n + 2][2 * half + e] * inv, w.oacc[n + 3][2 * half + e] * inv);
             if (warp == 0 && w.c == 0) {
-                const float tot = half ? t1 : t0, M = half ? w.M1 : w.M0;
-                const bool some = !(tot == 0.f);
+                const float M = half ? w.M1 : w.M0;
                 const float base = M == -INFINITY ? 0.f : M;
                 a.piece_ml[slot * C::kRows + h] =
                     some ? make_float2(base, base + log2f(tot)) : make_float2(-INFINITY, -INFINITY);
