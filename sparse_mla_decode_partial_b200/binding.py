@@ -513,15 +513,21 @@ def _want(t, dtype, name, device, shape=None):
         _on_device(t, name, device)
 
 
-def _new(shape, dtype, dev, stream):
-    """An empty tensor that a launch on ``stream`` uses: the allocator keeps its
-    memory from other streams until that launch is done, should it be dropped
-    before."""
-    t = torch.empty(*shape, dtype=dtype, device=dev)  # (separate sizes parse 0.7 us faster than a tuple)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
-        t.record_stream(stream)
+def _new(shape, dtype, dev, stream, returned=True):
+    """An empty tensor that a launch on ``stream`` uses.  It comes from that
+    stream's own memory: a block that the current stream has let go of may still
+    be written by work queued there, which nothing orders before the launch.
+    What is ``returned`` will be read on the current stream, which therefore holds
+    the memory too."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)  # (separate sizes parse 0.7 us faster than a tuple)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=dev)
+    if returned and here != stream:
+        t.record_stream(here)
     return t
 
 
@@ -615,7 +621,7 @@ def _queries(q):
 def _decode_out(dev, B, T, H, need, workspace, o, lse, stream):
     """Workspace and outputs of a decode, allocated where they are not given."""
     if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream)
+        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
     else:
         _want(workspace, torch.uint8, "workspace", dev)
     if o is None:
