@@ -152,6 +152,30 @@ def _on_device(t, name, device):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
+def _torch_stream(stream, dev):
+    """``stream`` (a torch stream, a handle, or None) as torch takes it."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream(stream), device=dev)
+
+
+def _new(shape, dtype, dev, stream, returned=True):
+    """An empty tensor that a launch on ``stream`` uses.  It comes from that
+    stream's own memory: a block that the current stream has let go of may still
+    be written by work queued there, which nothing orders before the launch.
+    What is ``returned`` will be read on the current stream, which therefore holds
+    the memory too."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=dev)  # (separate sizes parse 0.7 us faster than a tuple)
+    stream = _torch_stream(stream, dev)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=dev)
+    if returned and here != stream:
+        t.record_stream(here)
+    return t
+
+
 def choose_nsplit(B: int, T: int, H: int, K: int, sm_count: int = 0) -> int:
     return int(lib().smla_choose_nsplit(B, T, H, _k_in_range(K), sm_count))
 
@@ -185,11 +209,11 @@ def decode_partial(q, cache, page_table, idx, scale: float, nsplit: int, *, part
     B, T, H, K, pt_stride, num_pages = _decode_args(q, cache, page_table, idx)
     dev = q.device
     if part_o is None:
-        part_o = torch.empty((B, T, H, nsplit, DC), dtype=torch.float32, device=dev)
+        part_o = _new((B, T, H, nsplit, DC), torch.float32, dev, stream)
     if part_m is None:
-        part_m = torch.empty((B, T, H, nsplit), dtype=torch.float32, device=dev)
+        part_m = _new((B, T, H, nsplit), torch.float32, dev, stream)
     if part_lse is None:
-        part_lse = torch.empty((B, T, H, nsplit), dtype=torch.float32, device=dev)
+        part_lse = _new((B, T, H, nsplit), torch.float32, dev, stream)
     _need(part_o, torch.float32, "part_o", dev, (B, T, H, nsplit, DC))
     _need(part_m, torch.float32, "part_m", dev, (B, T, H, nsplit))
     _need(part_lse, torch.float32, "part_lse", dev, (B, T, H, nsplit))
@@ -212,9 +236,9 @@ def lse_combine(part_o, part_m, part_lse, *, o=None, lse=None, stream=None):
     if tuple(part_o.shape) != (B, T, H, S, DC) or part_lse.shape != part_m.shape:
         raise ValueError("partial shapes disagree")
     if o is None:
-        o = torch.empty((B, T, H, DC), dtype=torch.bfloat16, device=dev)
+        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = _new((B, T, H), torch.float32, dev, stream)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_lse_combine(_ptr(part_o), _ptr(part_m), _ptr(part_lse), B, T, H, S, _ptr(o),
@@ -235,12 +259,12 @@ def decode(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, workspac
         nsplit = choose_nsplit(B, T, H, K, 0)
     need = workspace_bytes(B, T, H, nsplit) if nsplit > 1 else 0
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     if o is None:
-        o = torch.empty((B, T, H, DC), dtype=torch.bfloat16, device=dev)
+        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = _new((B, T, H), torch.float32, dev, stream)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_decode(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
@@ -307,12 +331,12 @@ def decode_dense(q, cache, page_table, seq_lens, scale: float, nsplit: int = 0, 
         nsplit = dense_nsplit(B, T, H, K)
     need = dense_workspace_bytes(B, T, H, K, nsplit)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     if o is None:
-        o = torch.empty((B, T, H, DC), dtype=torch.bfloat16, device=dev)
+        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = _new((B, T, H), torch.float32, dev, stream)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_decode_dense(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
@@ -329,11 +353,11 @@ def decode_dense_partial(q, cache, page_table, seq_lens, scale: float, nsplit: i
     B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K)
     dev = q.device
     if part_o is None:
-        part_o = torch.empty((B, T, H, nsplit, DC), dtype=torch.float32, device=dev)
+        part_o = _new((B, T, H, nsplit, DC), torch.float32, dev, stream)
     if part_m is None:
-        part_m = torch.empty((B, T, H, nsplit), dtype=torch.float32, device=dev)
+        part_m = _new((B, T, H, nsplit), torch.float32, dev, stream)
     if part_lse is None:
-        part_lse = torch.empty((B, T, H, nsplit), dtype=torch.float32, device=dev)
+        part_lse = _new((B, T, H, nsplit), torch.float32, dev, stream)
     _need(part_o, torch.float32, "part_o", dev, (B, T, H, nsplit, DC))
     _need(part_m, torch.float32, "part_m", dev, (B, T, H, nsplit))
     _need(part_lse, torch.float32, "part_lse", dev, (B, T, H, nsplit))
@@ -381,7 +405,7 @@ def decode_host(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, o, 
         nsplit = choose_nsplit(B, T, H, K, 0)
     need = workspace_host_bytes(B, T, H, K, pt_stride, nsplit)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_decode_host(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
                                   _ptr(idx), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit),
@@ -429,11 +453,11 @@ def indexer_topk(q_index, w, k_index, page_table, n_vis, K: int, max_n: int, *, 
     dev = q_index.device
     K = _k_in_range(int(K))
     if out is None:
-        out = torch.empty((B, T, K), dtype=torch.int32, device=dev)
+        out = _new((B, T, K), torch.int32, dev, stream)
     _need(out, torch.int32, "out", dev, (B, T, K))
     if workspace is None:
-        workspace = torch.empty(max(16, indexer_workspace_bytes(B, T, max_n)), dtype=torch.uint8,
-                                device=dev)
+        workspace = _new((max(16, indexer_workspace_bytes(B, T, max_n)),), torch.uint8, dev, stream,
+                         returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_topk(_ptr(q_index), _ptr(w), _ptr(k_index), num_pages,
                                    _ptr(page_table), pt_stride, _ptr(n_vis), B, T, HI, int(max_n),
@@ -449,12 +473,14 @@ def indexer_scores(q_index, w, k_index, page_table, n_vis, max_n: int, *, scores
     B, T, HI, pt_stride, num_pages = _indexer_args(q_index, w, k_index, page_table, n_vis)
     dev = q_index.device
     if scores is None:
-        scores = torch.full((B, T, max(max_n, 1)), float("nan"), dtype=torch.float32, device=dev)
+        scores = _new((B, T, max(max_n, 1)), torch.float32, dev, stream)
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            scores.fill_(float("nan"))
     # rows of max_n scores, one per query token (nothing is written when max_n is 0)
     _need(scores, torch.float32, "scores", dev, (B, T, max_n) if max_n > 0 else None)
     if workspace is None:
-        workspace = torch.empty(max(16, indexer_workspace_bytes(B, T, 0)), dtype=torch.uint8,
-                                device=dev)
+        workspace = _new((max(16, indexer_workspace_bytes(B, T, 0)),), torch.uint8, dev, stream,
+                         returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_scores(_ptr(q_index), _ptr(w), _ptr(k_index), num_pages,
                                      _ptr(page_table), pt_stride, _ptr(n_vis), B, T, HI,
@@ -473,11 +499,11 @@ def indexer_select(scores, n_vis, K: int, *, out=None, workspace=None, stream=No
     _need(n_vis, torch.int32, "n_vis", dev, (B, T))
     K = _k_in_range(int(K))
     if out is None:
-        out = torch.empty((B, T, K), dtype=torch.int32, device=dev)
+        out = _new((B, T, K), torch.int32, dev, stream)
     _need(out, torch.int32, "out", dev, (B, T, K))
     if workspace is None:
-        workspace = torch.empty(max(16, indexer_select_workspace_bytes(B, T, max_n)),
-                                dtype=torch.uint8, device=dev)
+        workspace = _new((max(16, indexer_select_workspace_bytes(B, T, max_n)),), torch.uint8, dev, stream,
+                         returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_select(_ptr(scores), _ptr(n_vis), B, T, max_n, int(K),
                                      _ptr(workspace), workspace.numel(), _ptr(out),
@@ -511,24 +537,6 @@ def _want(t, dtype, name, device, shape=None):
             and (shape is None or t.shape == shape) and t.get_device() == device.index):
         _need(t, dtype, name, device, shape)
         _on_device(t, name, device)
-
-
-def _new(shape, dtype, dev, stream, returned=True):
-    """An empty tensor that a launch on ``stream`` uses.  It comes from that
-    stream's own memory: a block that the current stream has let go of may still
-    be written by work queued there, which nothing orders before the launch.
-    What is ``returned`` will be read on the current stream, which therefore holds
-    the memory too."""
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=dev)  # (separate sizes parse 0.7 us faster than a tuple)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
-    here = torch.cuda.current_stream(dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(*shape, dtype=dtype, device=dev)
-    if returned and here != stream:
-        t.record_stream(here)
-    return t
 
 
 def _paged(cache, width, dtype, dev, page_table, B):

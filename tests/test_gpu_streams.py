@@ -22,6 +22,8 @@ def check_beside_pending_work(call, scratch_bytes=0):
     want = [t.clone() for t in tensors(call(None))]
     sizes = [max(t.numel() * t.element_size(), 16) for t in want]
     side = torch.cuda.Stream()
+    torch.cuda._sleep(1)  # (loading a kernel waits for what runs, so this is done before)
+    torch.empty(16, dtype=torch.uint8, device="cuda").fill_(1)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     pending = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes + [max(scratch_bytes, 16)]]
@@ -68,6 +70,69 @@ def test_evict_plan():
     check_beside_pending_work(lambda s: binding.evict_plan(acc, n, 300, stream=s))
 
 
+def bf16_inputs():
+    lens = [900, 700]
+    paged = cu.Paged(lens, 2)
+    cache = cu.latents(paged.pages * 64, 3).view(paged.pages, 64, 576).cuda()
+    return paged.cuda, cache, torch.from_numpy(lists_for(lens, 1, 300, 1)).cuda(), cu.queries(2, 1, 16, 4).cuda()
+
+
+@pytest.mark.parametrize("nsplit", [1, 4])
+def test_decode(nsplit):
+    table, cache, idx, q = bf16_inputs()
+    check_beside_pending_work(lambda s: binding.decode(q, cache, table, idx, SCALE, nsplit, stream=s),
+                              binding.workspace_bytes(2, 1, 16, nsplit))
+
+
+def test_decode_partial_and_combine():
+    table, cache, idx, q = bf16_inputs()
+    call = lambda s: binding.decode_partial(q, cache, table, idx, SCALE, 4, stream=s)
+    check_beside_pending_work(call)
+    parts = call(None)
+    check_beside_pending_work(lambda s: binding.lse_combine(*parts, stream=s))
+
+
+def test_decode_dense():
+    table, cache, _, q = bf16_inputs()
+    lens = torch.tensor([[900], [700]], dtype=torch.int32).cuda()
+    check_beside_pending_work(lambda s: binding.decode_dense(q, cache, table, lens, SCALE, 4, K=900, stream=s),
+                              binding.dense_workspace_bytes(2, 1, 16, 900, 4))
+    check_beside_pending_work(lambda s: binding.decode_dense_partial(q, cache, table, lens, SCALE, 4, K=900, stream=s))
+
+
+def test_decode_host():
+    table, cache, idx, q = [t.cpu().pin_memory() if t.dtype != torch.bfloat16 or t.dim() == 4 else t for t in bf16_inputs()]
+    o, lse = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16).pin_memory(), torch.zeros(2, 1, 16).pin_memory()
+
+    def call(s):
+        binding.decode_host(q, cache, table, idx, SCALE, 4, o=o, lse=lse, stream=s)
+        torch.cuda.synchronize() if s is None else s.synchronize()
+        return o, lse
+
+    check_beside_pending_work(call, binding.workspace_host_bytes(2, 1, 16, 300, table.shape[1], 4))
+
+
+def test_indexer():
+    table = bf16_inputs()[0]
+    g = torch.Generator().manual_seed(5)
+    keys = torch.randn(int(table.max()) + 1, 64, 128, generator=g).to(torch.bfloat16).cuda()
+    q, w = torch.randn(2, 1, 8, 128, generator=g).to(torch.bfloat16).cuda(), torch.rand(2, 1, 8, generator=g).cuda()
+    n = torch.tensor([[900], [700]], dtype=torch.int32).cuda()
+    check_beside_pending_work(lambda s: binding.indexer_topk(q, w, keys, table, n, 128, 900, stream=s),
+                              binding.indexer_workspace_bytes(2, 1, 900))
+    check_beside_pending_work(lambda s: binding.indexer_scores(q, w, keys, table, n, 900, stream=s),
+                              binding.indexer_workspace_bytes(2, 1, 0))
+    scores = binding.indexer_scores(q, w, keys, table, n, 900)
+    check_beside_pending_work(lambda s: binding.indexer_select(scores, n, 128, stream=s),
+                              binding.indexer_select_workspace_bytes(2, 1, 900))
+
+
+def test_the_default_stream_given_as_zero():
+    table, cache, idx, q = bf16_inputs()
+    want, got = (binding.decode(q, cache, table, idx, SCALE, 4, stream=s) for s in (None, 0))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_a_stream_given_by_its_handle():
     table, cache, idx, q = q4_inputs()
     check_beside_pending_work(lambda s: binding.decode_q4(q, cache, table, idx, SCALE, 1,
@@ -81,6 +146,7 @@ def test_outputs_that_the_caller_still_reads_stay_theirs():
     want = binding.decode_q4(q, cache, table, idx, SCALE, 1)[0].clone()
     other = -q
     side = torch.cuda.Stream()
+    torch.cuda._sleep(1)
     torch.cuda.synchronize()
     o, _ = binding.decode_q4(q, cache, table, idx, SCALE, 1, stream=side)
     torch.cuda.current_stream().wait_stream(side)
