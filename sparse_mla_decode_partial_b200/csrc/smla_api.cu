@@ -1185,19 +1185,14 @@ void set_partials(PartialParams *p, void *workspace, size_t n) {
 // Query rows that smla_partial_q4.cuh takes at once.
 constexpr int kQ4Rows = smla::Q4Cfg::kRows;
 
-template <bool DIRECT, bool SHORT>
-smla_status launch_q4_small(const PartialParams &p, int grid, cudaStream_t st) {
-    using C = smla::Q4Cfg;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_q4_sparse_kernel<DIRECT, SHORT>), C::kSmemBytes);
-    if (e != cudaSuccess) return cuda_fail(e);
-    e = launch_dependent(smla::smla_q4_sparse_kernel<DIRECT, SHORT>, grid, C::kThreads, C::kSmemBytes, st, p);
-    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
-}
-
 template <bool DIRECT>
 smla_status launch_q4_sparse(const PartialParams &p, int grid, cudaStream_t st) {
     if (p.H > kQ4Rows) return launch_tc<DIRECT, true>(p, grid, st);
-    return p.K <= smla::kQ4Short ? launch_q4_small<DIRECT, true>(p, grid, st) : launch_q4_small<DIRECT, false>(p, grid, st);
+    using C = smla::Q4Cfg;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_q4_sparse_kernel<DIRECT>), C::kSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = launch_dependent(smla::smla_q4_sparse_kernel<DIRECT>, grid, C::kThreads, C::kSmemBytes, st, p);
+    return e == cudaSuccess ? SMLA_OK : cuda_fail(e);
 }
 
 // Splits of an index list over the 4-bit cache, up to 16 heads.  Measured: a
@@ -1390,10 +1385,9 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
         a.piece_ml = reinterpret_cast<float2 *>(ws + d.off_ml);
         a.prefix = reinterpret_cast<int *>(ws + d.off_prefix);
         using C = smla::Q4Cfg;
-        const auto kernel = K <= smla::kQ4Short ? smla::smla_q4_dense_kernel<true> : smla::smla_q4_dense_kernel<false>;
-        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::kSmemBytes);
+        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(&smla::smla_q4_dense_kernel), C::kSmemBytes);
         if (e != cudaSuccess) return cuda_fail(e);
-        e = launch_dependent(kernel, a.grid, C::kThreads, C::kSmemBytes, s, a);
+        e = launch_dependent(smla::smla_q4_dense_kernel, a.grid, C::kThreads, C::kSmemBytes, s, a);
         if (e != cudaSuccess) return cuda_fail(e);
         const int rows = B * T * H;
         e = rows <= current_device_sms() / 2

@@ -23,11 +23,13 @@
 // Running maxima: each warp keeps one per query row over its own rows, rounded
 // up to an integer (log2 units), so that bringing its P to the common maximum
 // is a multiplication by a power of two, exact in bf16: P is rounded once.
-// SHORT (at most kQ4Short rows): the output is divided by the sum of the rounded P
-// (lse is that of the others), so that a row which dominates is not off by its P's
-// rounding.  One row comes out bit for bit; 64 rows are off by 2.2e-3 of o in place
-// of 2.5e-3 (its own rounding is 1.7e-3), 2048 by 1.93e-3 in place of 1.95e-3.  It
-// costs 3.5%: 32 sequences as below took 112.5 us.
+// The output is divided by the sum of the rounded P (lse is that of the others),
+// so that a row which dominates is not off by its P's rounding, whatever the
+// list's width or the bound K: one row comes out bit for bit, 64 rows are off by
+// 2.2e-3 of o in place of 2.5e-3 (its own rounding is 1.7e-3), 2048 by 1.93e-3 in
+// place of 1.95e-3.  A product with ones adds them up beside the maxima it is
+// relative to: 111.0 us where the sum of the others takes 108.6 (32 sequences as
+// below; adding up in registers 113.1), 37.1 and 36.8 (64 lists).
 // Rows 416 bytes apart: the lane-to-row map below keeps every shared load free
 // of bank conflicts without padding, so a page of the cache lands by one bulk
 // copy.
@@ -50,8 +52,6 @@
 #include "smla_tc_ptx.cuh"
 
 namespace smla {
-
-constexpr int kQ4Short = 512;
 
 struct Q4Cfg {
     static constexpr int kThreads = 128;
@@ -196,14 +196,12 @@ __device__ __forceinline__ void q4_scores(uint32_t q, uint32_t rows, int lane, f
 }
 
 // One warp's share of a CTA: scores of 16 rows, 128 output columns.
-template <bool SHORT>
 struct Q4Consumer {
     int warp, lane, r, c;
     float oacc[16][4];
     float mw0, mw1;    // running max (an integer or -inf) of query rows r, r + 8 over this warp's cache rows
     float l0, l1;      // this lane's part of sum exp2(s - mw)
-    uint32_t own[4];   // SHORT: this warp's P, relative to mw, and
-    float racc[4];     // sums of it over the tiles, relative to M (rows r, r, r + 8, r + 8)
+    float racc[4];     // sums of this warp's rounded P relative to mw: query row r at [0], r + 8 at [2]
     float M0, M1;      // the CTA's running max, what oacc is relative to
 
     __device__ __forceinline__ void init(int warp_, int lane_) {
@@ -216,7 +214,7 @@ struct Q4Consumer {
     __device__ __forceinline__ void reset() {
         mw0 = mw1 = M0 = M1 = -INFINITY;
         l0 = l1 = 0.f;
-        if (SHORT) racc[0] = racc[1] = racc[2] = racc[3] = 0.f;
+        racc[0] = racc[1] = racc[2] = racc[3] = 0.f;
 #pragma unroll
         for (int n = 0; n < 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
     }
@@ -232,8 +230,11 @@ struct Q4Consumer {
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
         const float n0 = fmaxf(mw0, ceilf(x0)), n1 = fmaxf(mw1, ceilf(x1));
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-        l0 *= fast_exp2(mw0 - u0);  // 2^-inf = 0 before the first visible row
-        l1 *= fast_exp2(mw1 - u1);
+        const float f0 = fast_exp2(mw0 - u0), f1 = fast_exp2(mw1 - u1);  // 2^-inf = 0 before the first visible row
+        l0 *= f0;
+        l1 *= f1;
+        racc[0] *= f0;
+        racc[2] *= f1;
         mw0 = n0;
         mw1 = n1;
         uint32_t a[4];
@@ -246,10 +247,7 @@ struct Q4Consumer {
             a[2 * i] = pack_bf16x2(p00, p01);
             a[2 * i + 1] = pack_bf16x2(p10, p11);
         }
-        if (SHORT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) own[i] = a[i];
-        }
+        mma_bf16_16816(racc, a[0], a[1], a[2], a[3], 0x3F803F80u, 0x3F803F80u);  // a product with ones adds them up
         __syncwarp();  // every lane has read the rope bytes
         const uint32_t mine = tile + 16 * warp * kQ4RowBytes + kQ4OffRope;
         sts_16(mine + (lane >> 1) * kQ4RowBytes + 16 * (lane & 1), a[0], a[1], a[2], a[3]);
@@ -280,17 +278,8 @@ struct Q4Consumer {
                 oacc[n][2] *= a1;
                 oacc[n][3] *= a1;
             }
-            if (SHORT) {
-                racc[0] *= a0;
-                racc[2] *= a1;
-            }
             M0 = n0;
             M1 = n1;
-        }
-        if (SHORT) {  // a product with ones adds this warp's rounded P up
-            const uint32_t f0 = bf16x2_pow2(mw0 - M0), f1 = bf16x2_pow2(mw1 - M1);
-            mma_bf16_16816(racc, bf16x2_mul(own[0], f0), bf16x2_mul(own[1], f1), bf16x2_mul(own[2], f0),
-                           bf16x2_mul(own[3], f1), 0x3F803F80u, 0x3F803F80u);
         }
         const int ra = q4_row_of(2 * c), rb = q4_row_of(2 * c + 1);
 #pragma unroll
@@ -326,8 +315,8 @@ struct Q4Consumer {
     }
 
     // Total weight of query rows r, r + 8 relative to M, the same in every lane
-    // of a row, and (SHORT) that of the rounded P.  scratch: float2 [2][4][16] in
-    // shared memory; the CTA synchronises.
+    // of a row, and that of the rounded P.  scratch: float2 [2][4][16] in shared
+    // memory; the CTA synchronises.
     __device__ __forceinline__ void totals(float2 *scratch, float &t0, float &t1, float &u0, float &u1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -336,22 +325,20 @@ struct Q4Consumer {
         if (c == 0) {
             scratch[16 * warp + r] = make_float2(mw0, l0);
             scratch[16 * warp + r + 8] = make_float2(mw1, l1);
-            if (SHORT) scratch[64 + 16 * warp + r] = make_float2(racc[0], racc[2]);
+            scratch[64 + 16 * warp + r] = make_float2(racc[0], racc[2]);
         }
         __syncthreads();
         t0 = t1 = u0 = u1 = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float2 x = scratch[16 * w + r], y = scratch[16 * w + r + 8];
-            // a warp that saw nothing has l = 0; one whose every score was NaN
-            // keeps its NaN
-            t0 += x.x == -INFINITY ? x.y : x.y * fast_exp2(x.x - M0);
-            t1 += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M1);
-            if (SHORT) {
-                const float2 z = scratch[64 + 16 * w + r];
-                u0 += z.x;
-                u1 += z.y;
-            }
+            const float2 x = scratch[16 * w + r], y = scratch[16 * w + r + 8], z = scratch[64 + 16 * w + r];
+            // a warp that saw nothing has sums of 0; one whose every score was
+            // NaN keeps its NaN
+            const float f0 = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M0), f1 = y.x == -INFINITY ? 1.f : fast_exp2(y.x - M1);
+            t0 += x.y * f0;
+            t1 += y.y * f1;
+            u0 += z.x * f0;
+            u1 += z.y * f1;
         }
     }
 };
@@ -382,7 +369,7 @@ __device__ __forceinline__ void q4_stage_q(uint8_t *dst, const __nv_bfloat16 *q,
 // list starts its pipeline anew.  A cluster of four splits that merge in
 // distributed shared memory took 35.8, but of two 60.8 against 43.7 and of sixteen
 // (15 lists) 23.5 against 14.9.
-template <bool DIRECT, bool SHORT>
+template <bool DIRECT>
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sparse_kernel(const PartialParams p) {
     using C = Q4Cfg;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -420,7 +407,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
                      : "memory");
     };
 
-    Q4Consumer<SHORT> w;
+    Q4Consumer w;
     w.init(warp, lane);
     bool staged = false;
     int it = 0;  // tiles so far: ring position
@@ -468,8 +455,8 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_sp
         const float tot = half ? t1 : t0, M = half ? w.M1 : w.M0;
         const bool some = !(tot == 0.f);  // NaN counts
         const size_t row = (size_t)bt * p.H + h;
-        const float sum = SHORT ? (half ? u1 : u0) : tot;  // what the output is divided by
-        const float inv = DIRECT ? (some ? 1.f / sum : 0.f) : SHORT ? (some ? tot / sum : 1.f) : 1.f;
+        const float sum = half ? u1 : u0;  // what the output is divided by
+        const float inv = !some ? 0.f : DIRECT ? 1.f / sum : tot / sum;
         // n8 tile n of the accumulators is column 128 warp + 16 (2 c + e) + n
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -594,7 +581,6 @@ __device__ __forceinline__ void q4_copy_page(const PartialParams &p, int pg, uin
              (uint32_t)Q4Cfg::kStageBytes, bar);
 }
 
-template <bool SHORT>
 __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_dense_kernel(const Q4Params a) {
     using C = Q4Cfg;
     const PartialParams &p = a.p;
@@ -614,7 +600,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
     const Q4Run run = q4_find_run<C::kTile>(p, a.grid, 1, a.prefix, scratch);
     const int nrows = p.dense_t * p.dense_h;
     int b = run.b, tile0 = run.tile;
-    Q4Consumer<SHORT> w;
+    Q4Consumer w;
     w.init(warp, lane);
     int it = 0;
     for (long long at = run.begin; at < run.end && b < p.B; ++b, tile0 = 0) {
@@ -689,7 +675,7 @@ __global__ void __launch_bounds__(Q4Cfg::kThreads, Q4Cfg::kMinBlocks) smla_q4_de
             if (h >= nrows) continue;
             const float tot = half ? t1 : t0;
             const bool some = !(tot == 0.f);
-            const float inv = SHORT ? (some ? tot / (half ? u1 : u0) : 1.f) : 1.f;
+            const float inv = some ? tot / (half ? u1 : u0) : 0.f;
             float *dst = a.piece_o + (slot * C::kRows + h) * kDc + 128 * warp + 32 * w.c;
 #pragma unroll
             for (int e = 0; e < 2; ++e)

@@ -498,3 +498,52 @@ def test_extreme_scores(fill_value):
         q = torch.ones(1, 1, H, 576).to(torch.bfloat16)
         o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, torch.tensor([[64]], dtype=torch.int32).cuda(), 1.0)
         cu.check_attention(o, lse, q, lambda b, t: vals, 1.0, "extreme")
+
+
+def one_row_of(cache, table, pos, H):
+    """The latents at pos [B, T] as the o of queries that see only them."""
+    B, T = pos.shape
+    return binding.q4_read(cache, table, pos)[:, :, None, :512].expand(B, T, H, 512)
+
+
+@pytest.mark.parametrize("H", [3, 16, 40])
+@pytest.mark.parametrize("nsplit", [0, 1, 5])
+def test_one_row_of_a_wide_list_comes_out_as_it_is(H, nsplit):
+    """What a list of one row gives does not hang on the list's width or on where in it the row stands."""
+    paged = cu.Paged([90, 70], 1)
+    cache, _ = fill(paged, [90, 70], 2)
+    idx = torch.full((2, 3, 2048), -1, dtype=torch.int32)
+    pos = torch.tensor([[77, 3, 89], [0, 64, 69]], dtype=torch.int32)
+    for b in range(2):
+        for t, at in enumerate((0, 1000 + b, 2047)):
+            idx[b, t, at] = pos[b, t]
+    o, lse = binding.decode_q4(cu.queries(2, 3, H, 3).cuda(), cache, paged.cuda, idx.cuda(), SCALE, nsplit)
+    assert torch.equal(o, one_row_of(cache, paged.cuda, pos.cuda(), H))
+
+
+@pytest.mark.parametrize("T,H", [(1, 3), (1, 16), (2, 8), (1, 40), (2, 40)])
+def test_one_visible_position_comes_out_as_it_is(T, H):
+    """Neither a bound above every length nor a longer neighbour or a longer token of the same sequence changes it."""
+    paged = cu.Paged([4000, 4000, 90], 1)
+    cache, _ = fill(paged, None, 2)
+    table, q = paged.cuda, cu.queries(3, T, H, 3).cuda()
+    want = one_row_of(cache, table, torch.zeros(3, T, dtype=torch.int32).cuda(), H)
+    one = torch.ones(3, T, dtype=torch.int32).cuda()
+    assert torch.equal(binding.decode_dense_q4(q, cache, table, one, SCALE, K=4096)[0], want)
+    one[1], one[0, -1] = 4000, 4000 if T > 1 else 1
+    o = binding.decode_dense_q4(q, cache, table, one, SCALE, K=4096)[0]
+    seen = one.cpu() == 1
+    assert torch.equal(o[seen], want[seen])
+
+
+@pytest.mark.parametrize("T,H", [(1, 16), (3, 4)])
+def test_the_bound_alone_changes_nothing(T, H):
+    """Up to 16 query rows: the same bits with the least bound and with larger ones."""
+    lens = torch.tensor([[300 - T + t + 1 for t in range(T)], [70 + t for t in range(T)]], dtype=torch.int32).cuda()
+    paged = cu.Paged([300, 80], 1, extra=1)
+    cache, _ = fill(paged, None, 2)
+    q = cu.queries(2, T, H, 3).cuda()
+    want = binding.decode_dense_q4(q, cache, paged.cuda, lens, SCALE, 4, K=300)
+    for K in (512, 513, 40000):
+        got = binding.decode_dense_q4(q, cache, paged.cuda, lens, SCALE, 4, K=K)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
