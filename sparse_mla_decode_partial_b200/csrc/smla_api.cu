@@ -1642,8 +1642,10 @@ smla_status smla_evict_apply(const int32_t *src, int B, int K, const int32_t *pa
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (2 * 16 * p.total <= smla::kApplyBulkBytes) {
-        // two waves of the CTAs that fit: the second evens out what the first left
-        const long long most = 16ll * current_device_sms();
+        // a little more than two waves of the CTAs that fit: what starts later
+        // evens out what the first left.  (80000 rows of 1408 bytes, 16 CTAs per SM
+        // 40.6 us, 14 42.5; eight at a time and eight in all 45.9.)
+        const long long most = (2ll * smla::kApplyBlocks + 2) * current_device_sms();
         e = launch_dependent(smla::smla_evict_apply_bulk_kernel, (int)std::min(units, most), 32,
                              smla::kApplyBulkBytes, st, p);
         return e == cudaSuccess ? SMLA_OK : cuda_fail(e);

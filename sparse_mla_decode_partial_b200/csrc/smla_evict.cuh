@@ -352,10 +352,14 @@ __device__ __forceinline__ EvictMove evict_move(const EvictApplyParams &p, long 
 // Rows that fit shared memory several times over (all real caches): one warp per
 // CTA, a lane per move.  Each lane has its row's pieces copied in by bulk copies
 // and, when the warp's have landed, out again: a few instructions per row, and
-// 28 KB per CTA, eight CTAs per SM, in flight.  (Moving 16-byte pieces through
+// 28 KB per CTA, seven CTAs per SM, in flight.  (Moving 16-byte pieces through
 // registers took 65 instructions per 512 bytes, and 51 us where this takes 41,
-// 80000 rows of 1408 bytes: 5.5 TB/s.)
+// 80000 rows of 1408 bytes: 5.5 TB/s.  Eight CTAs of nineteen such rows: 41.3 us
+// where seven of twenty take 40.6.)
 constexpr int kApplyBulkBytes = 28160;  // twenty rows of 1152 + 256 bytes
+constexpr int kApplyBlocks = 7;         // per SM; each with 128 bytes for the barrier
+static_assert(kApplyBlocks * (kApplyBulkBytes + 128 + 1024) <= 233472 &&
+              (kApplyBlocks + 1) * (kApplyBulkBytes + 128 + 1024) > 233472, "CTAs per SM");
 __global__ void __launch_bounds__(32) smla_evict_apply_bulk_kernel(const EvictApplyParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar;
