@@ -553,8 +553,8 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  *      n_new int32 [B]: m.
  *      acc_new fp32, pos_new int32 [B, max_n], either may be NULL: acc and pos
  *           carried along (slot i from src[b, i]); 0 and -1 from m on.
- *    src, n_new, acc_new and pos_new must overlap neither one another nor acc,
- *    pos and n (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
+ *    src, n_new, acc_new, pos_new and a workspace that is used must overlap neither
+ *    one another nor acc, pos and n (SMLA_ERR_INVALID_ARG).  max_n is at most SMLA_EVICT_MAX_N.  An n[b]
  *    outside [0, max_n] is clamped and counted.  workspace is used only where
  *    pos_new is NULL (it may be NULL otherwise): device, 16-B aligned, at least
  *    smla_evict_workspace_bytes(B, max_n).

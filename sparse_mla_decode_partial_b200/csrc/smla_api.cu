@@ -1566,19 +1566,17 @@ smla_status smla_evict_plan(const float *acc, const int32_t *pos, const int32_t 
     if (!aligned(acc, 4) || !aligned(pos, 4) || !aligned(n, 4) || !aligned(src, 4) || !aligned(n_new, 4) ||
         !aligned(acc_new, 4) || !aligned(pos_new, 4))
         return SMLA_ERR_MISALIGNED;
-    const size_t cells = (size_t)B * max_n * 4;
+    const size_t cells = (size_t)B * max_n * 4, scratch = pos_new == nullptr ? smla_evict_workspace_bytes(B, max_n) : 0;
+    const smla_status st = check_workspace(workspace, workspace_bytes, scratch);
+    if (st != SMLA_OK) return st;
     const struct {
         const void *at;
         size_t bytes;
-    } buf[] = {{src, (size_t)B * K * 4}, {n_new, (size_t)B * 4}, {acc_new, cells}, {pos_new, cells},  // outputs
+    } buf[] = {{src, (size_t)B * K * 4}, {n_new, (size_t)B * 4}, {acc_new, cells}, {pos_new, cells}, {workspace, scratch},  // written
                {acc, cells}, {pos, cells}, {n, (size_t)B * 4}};
-    for (int i = 0; i < 4; ++i)
-        for (int j = i + 1; j < 7; ++j)
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 8; ++j)
             if (overlap(buf[i].at, buf[i].bytes, buf[j].at, buf[j].bytes)) return SMLA_ERR_INVALID_ARG;
-    if (pos_new == nullptr) {
-        const smla_status st = check_workspace(workspace, workspace_bytes, smla_evict_workspace_bytes(B, max_n));
-        if (st != SMLA_OK) return st;
-    }
     smla::EvictPlanParams p{};
     p.acc = acc;
     p.pos = pos;

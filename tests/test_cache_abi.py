@@ -165,3 +165,10 @@ def test_binding_refuses_wrong_tensors():
         binding.evict_plan(table, i32, 4)
     with pytest.raises(TypeError):
         binding.evict_apply(table.long(), table, (cache,))
+
+
+@pytest.mark.parametrize("at", [FAKE, FAKE + 2048 + 384, FAKE + 4096, FAKE + 8192 + 784, FAKE + 32768 - 768, FAKE + 65536 - 1008])
+def test_plan_refuses_a_workspace_that_overlaps(lib, at):
+    """acc (also pos), src, n_new, acc_new, pos and n, each in its first or last bytes; unused, it may lie anywhere."""
+    args = dict(ws=at, pos=FAKE + 32768, n=FAKE + 65536)
+    assert plan(lib, pos_new=None, **args) == INVALID
