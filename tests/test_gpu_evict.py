@@ -430,3 +430,127 @@ def test_a_cache_lives_through_steps_and_evictions(q4):
         at = paged.rows(b, range(len(held[b])))
         got = cu.values(raw.numpy().reshape(-1, cu.ROW)[at]) if q4 else cu.f64(raw.view(-1, 576)[at])
         np.testing.assert_array_equal(got, np.stack([v for _, v in held[b]]))
+
+
+# ---------------------------------------------------------------- long sequences
+def check_weights_on_the_gpu(acc, before, q, lse, lens, values, what):
+    """check_weights() for long sequences: the same definition and bound in 64 bits by
+    torch, every position; values [B] of [n, 576]."""
+    B, T, H = lse.shape
+    q, lse = q.double(), lse.double()
+    want, tol = before.double(), torch.zeros_like(before, dtype=torch.float64)
+    for b in range(B):
+        kv = values[b].double()
+        for t in range(T):
+            n = int(lens[b, t])
+            s = q[b, t] @ kv[:n].T * SCALE
+            ds = 580 * 2.0 ** -23 * SCALE * (q[b, t].abs() @ kv[:n].abs().T) + 2.0 ** -22 * (s.abs() + lse[b, t].abs()[:, None] + 1)
+            w = torch.exp(s - lse[b, t][:, None])
+            want[b, :n] += w.sum(0)
+            tol[b, :n] += (w * (2 * ds + 2.0 ** -20 + 2.0 ** -23 * T * H)).sum(0)
+    tol += 2.0 ** -23 * want.abs() + 1e-37
+    off = (acc.double() - want).abs()
+    assert (off <= tol).all(), f"{what}: {(off > tol).sum().item()} off, worst {(off / tol).max().item():.3g} x the bound"
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("T,H", [(1, 16), (3, 8), (4, 16), (9, 8), (2, 48), (16, 8), (25, 8), (5, 64)])
+def test_weights_over_long_sequences(T, H, q4):
+    """Every block walks several steps of a sequence: the ring, the accumulators and the
+    parts of a score come round again, once and in further passes."""
+    lens = torch.tensor([[65111 - T + t + 1 for t in range(T)], [30001 - 7 * t for t in range(T)]], dtype=torch.int32)
+    paged = cu.Paged([65111, 30001], T)
+    pages = sum(-(-n // 64) for n in (65111, 30001))
+    assert pages >= 2 * 3 * torch.cuda.get_device_properties(0).multi_processor_count  # three steps of two pages each
+    table = paged.cuda
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    rows = (torch.randn(paged.pages * 64, 576, device="cuda", generator=g) * 0.7).to(torch.bfloat16)
+    if q4:
+        cache = torch.zeros(paged.pages, 64, cu.ROW, dtype=torch.uint8, device="cuda")
+        binding.q4_append(rows, cache, torch.arange(paged.pages, dtype=torch.int32)[None].cuda(),
+                          torch.tensor([0, len(rows)], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda())
+        values = [binding.q4_read(cache, table[b:b + 1], torch.arange(n, dtype=torch.int32)[None].cuda())[0]
+                  for b, n in enumerate((65111, 30001))]
+    else:
+        cache = rows.view(paged.pages, 64, 576)
+        values = [rows[torch.from_numpy(paged.rows(b, range(n))).cuda()] for b, n in enumerate((65111, 30001))]
+    q = (torch.randn(2, T, H, 576, device="cuda", generator=g) * 1.5).to(torch.bfloat16)
+    lse = torch.rand(2, T, H, device="cuda", generator=g) + 4.0
+    before = torch.rand(2, 65111, device="cuda", generator=g)
+    acc, again = before.clone(), before.clone()
+    for x in (acc, again):
+        binding.evict_accumulate(q, cache, table, lens.cuda(), lse, SCALE, x)
+    assert torch.equal(acc, again) and torch.equal(acc[1, 30001:], before[1, 30001:])
+    check_weights_on_the_gpu(acc, before, q, lse, lens, values, f"T {T} H {H} q4 {q4}")
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_steps_and_evictions_queued_without_a_synchronisation(q4):
+    """The device calls of all steps stand in the stream before the first of them
+    runs; what each gave is checked afterwards."""
+    B, H, budget, room, steps = 3, 8, 96, 256, 4
+    paged = cu.Paged([room] * B, 7)
+    table = paged.cuda
+    rng = np.random.default_rng(5)
+    new = [[int(rng.integers(40, 90)) for _ in range(B)] for _ in range(steps)]
+    rows = [cu.latents(sum(k), 100 + s) for s, k in enumerate(new)]
+    q = [cu.queries(B, 1, H, 200 + s) for s in range(steps)]
+    count = [[0] * B]  # slots in use before each step
+    for k in new:
+        count.append([min(a + c, budget) for a, c in zip(count[-1], k)])
+    seen = [sum(new[s][b] for s in range(step)) if step else 0 for step in range(steps + 1) for b in range(B)]
+    seen = [seen[B * s:B * s + B] for s in range(steps + 1)]  # tokens before each step
+    dev = []
+    for s in range(steps):
+        offs = torch.tensor(np.concatenate([[0], np.cumsum(new[s])]), dtype=torch.int32).cuda()
+        start = torch.tensor(count[s], dtype=torch.int32).cuda()
+        flat = torch.cat([torch.from_numpy(paged.rows(b, range(count[s][b], count[s][b] + new[s][b]))) for b in range(B)]).cuda()
+        slot = torch.cat([b * room + count[s][b] + torch.arange(new[s][b]) for b in range(B)]).cuda()
+        tok = torch.cat([seen[s][b] + torch.arange(new[s][b]) for b in range(B)]).int().cuda()
+        dev.append((rows[s].cuda(), offs, start, flat, slot, tok, q[s].cuda(), start + torch.tensor(new[s], dtype=torch.int32).cuda()))
+    cache = torch.zeros(paged.pages, 64, cu.ROW if q4 else 576, dtype=torch.uint8 if q4 else torch.bfloat16, device="cuda")
+    acc, pos = torch.zeros(B, room).cuda(), torch.full((B, room), -1, dtype=torch.int32).cuda()
+    got = []
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        torch.cuda._sleep(100_000_000)  # some 50 ms: the queue fills meanwhile
+        for s, (r, offs, start, flat, slot, tok, qs, n) in enumerate(dev):
+            if q4:
+                binding.q4_append(r, cache, table, offs, start)
+            else:
+                cache.view(-1, 576).index_copy_(0, flat, r)
+            pos.view(-1).index_copy_(0, slot, tok)
+            lens, most = n[:, None].contiguous(), max(a + c for a, c in zip(count[s], new[s]))
+            o, lse = (binding.decode_dense_q4 if q4 else binding.decode_dense)(qs, cache, table, lens, SCALE, K=most)
+            before = acc.clone()
+            binding.evict_accumulate(qs, cache, table, lens, lse, SCALE, acc)
+            p = binding.evict_plan(acc, n, budget, pos=pos, n_sink=4, n_recent=32)
+            binding.evict_apply(p.src, table, (cache,))
+            got.append((o, lse, before, acc, pos, p))
+            acc, pos = p.acc, p.pos
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    held = [[] for _ in range(B)]
+    for s, (o, lse, before, acc, pos, p) in enumerate(got):
+        stored = cu.values(cu.quantise(rows[s])) if q4 else cu.f64(rows[s])
+        at = 0
+        for b in range(B):
+            held[b] += [(seen[s][b] + k, stored[at + k]) for k in range(new[s][b])]
+            at += new[s][b]
+            assert pos[b, :len(held[b])].tolist() == [h[0] for h in held[b]]
+        vals = [np.stack([v for _, v in h]) for h in held]
+        if q4:
+            cu.check_attention(o, lse, q[s], lambda b, t: vals[b], SCALE, f"step {s}")
+        check_weights(acc, before.double().cpu().numpy(), cu.f64(q[s]), lse.double().cpu().numpy(),
+                      np.array([[len(h)] for h in held]), lambda b, k: vals[b][:k], f"step {s}")
+        for b in range(B):
+            src = cu.plan(acc[b].cpu().tolist(), pos[b].tolist(), len(held[b]), budget, 4, 32)
+            np.testing.assert_array_equal(p.src[b, :len(src)].cpu().numpy(), src)
+            held[b] = [held[b][i] for i in src]
+    raw = cache.cpu()
+    for b in range(B):
+        at = paged.rows(b, range(len(held[b])))
+        have = cu.values(raw.numpy().reshape(-1, cu.ROW)[at]) if q4 else cu.f64(raw.view(-1, 576)[at])
+        np.testing.assert_array_equal(have, np.stack([v for _, v in held[b]]))

@@ -547,3 +547,26 @@ def test_the_bound_alone_changes_nothing(T, H):
     for K in (512, 513, 40000):
         got = binding.decode_dense_q4(q, cache, paged.cuda, lens, SCALE, 4, K=K)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_dense_more_pieces_than_the_combine_has_threads():
+    """600 blocks share the 610 tiles of one sequence among empty ones: 600 pieces, where
+    the combine's 512 threads take one each.  (Few rows, which four blocks join, have
+    at most two blocks per SM to be cut by, so they never have as many.)"""
+    blocks, tiles = 600, -(-39000 // 64)
+    pieces = min(blocks, tiles)
+    assert 2 * torch.cuda.get_device_properties(0).multi_processor_count <= blocks and pieces > 512
+    run_dense([[0]] * 400 + [[39000]] + [[0]] * 199, 2, 0, seed=1)
+    run_dense([[0, 0]] * 599 + [[38999, 39000]], 8, 0, seed=2)
+
+
+@pytest.mark.parametrize("H", [24, 64])
+def test_dense_clamps_lengths_and_masks_unmapped_positions_of_many_rows(H):
+    paged = cu.Paged([128, 128], 1)
+    paged.table[1, 1] = -1
+    cache, vals = fill(paged, None, 2)
+    q = cu.queries(2, 1, H, 3)
+    o, lse = binding.decode_dense_q4(q.cuda(), cache, paged.cuda, torch.tensor([[-4], [128]], dtype=torch.int32).cuda(),
+                                     SCALE, 1, K=128)
+    assert binding.check_device(clear=True)[0] == 5
+    cu.check_attention(o, lse, q, lambda b, t: vals[paged.rows(b, range(64 * b))], SCALE, "unmapped")
