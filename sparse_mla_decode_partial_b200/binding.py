@@ -299,7 +299,15 @@ def dense_workspace_bytes(B: int, T: int, H: int, K: int, nsplit: int) -> int:
     return int(lib().smla_dense_workspace_bytes(B, T, H, K, nsplit))
 
 
-def _dense_args(q, cache, page_table, seq_lens, K):
+def _longest(seq_lens, stream) -> int:
+    """The longest length, as it stands on the stream of the launch."""
+    if not seq_lens.numel():
+        return 0
+    with torch.cuda.stream(_torch_stream(stream, seq_lens.device)):
+        return int(seq_lens.max().item())
+
+
+def _dense_args(q, cache, page_table, seq_lens, K, stream):
     _need(q, torch.bfloat16, "q")
     dev = q.device
     _need(cache, torch.bfloat16, "cache", dev)
@@ -315,7 +323,7 @@ def _dense_args(q, cache, page_table, seq_lens, K):
     if cache.numel() % (PAGE_SIZE * D):
         raise ValueError("cache must be [num_pages, 64, 576]")
     if K is None:
-        K = int(seq_lens.max().item()) if seq_lens.numel() else 0
+        K = _longest(seq_lens, stream)
     return B, T, H, _k_in_range(int(K)), page_table.shape[1], cache.numel() // (PAGE_SIZE * D)
 
 
@@ -325,7 +333,7 @@ def decode_dense(q, cache, page_table, seq_lens, scale: float, nsplit: int = 0, 
     positions 0 .. seq_lens[b, t] - 1 of sequence b.  K defaults to the longest
     length (read from seq_lens, which synchronises); pass it to stay
     asynchronous.  Returns (o bf16 [B,T,H,512], lse fp32 [B,T,H])."""
-    B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K)
+    B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K, stream)
     dev = q.device
     if nsplit == 0:
         nsplit = dense_nsplit(B, T, H, K)
@@ -350,7 +358,7 @@ def decode_dense_partial(q, cache, page_table, seq_lens, scale: float, nsplit: i
                          part_o=None, part_m=None, part_lse=None, stream=None):
     """Partial pass of the dense variant; returns (part_o [B,T,H,S,512],
     part_m [B,T,H,S], part_lse [B,T,H,S])."""
-    B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K)
+    B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K, stream)
     dev = q.device
     if part_o is None:
         part_o = _new((B, T, H, nsplit, DC), torch.float32, dev, stream)
@@ -671,7 +679,7 @@ def decode_dense_q4(q, cache, page_table, seq_lens, scale: float, nsplit: int = 
     num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
     _want(seq_lens, torch.int32, "seq_lens", dev, (B, T))
     if K is None:
-        K = int(seq_lens.max().item()) if seq_lens.numel() else 0
+        K = _longest(seq_lens, stream)
     K = _k_in_range(int(K))
     nsplit = int(nsplit)
     need = dense_q4_workspace_bytes(B, T, H, K, nsplit) if workspace is None else 0

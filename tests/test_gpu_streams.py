@@ -156,3 +156,22 @@ def test_outputs_that_the_caller_still_reads_stay_theirs():
     binding.decode_q4(other, cache, table, idx, SCALE, 1, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+@pytest.mark.parametrize("H", [16, 40])
+@pytest.mark.parametrize("q4", [False, True])
+def test_lengths_that_the_side_stream_has_still_to_write(q4, H):
+    """Without K the bound is read from the lengths as they stand on the call's stream."""
+    table, cache = (q4_inputs() if q4 else bf16_inputs())[:2]
+    decode = binding.decode_dense_q4 if q4 else binding.decode_dense
+    q, lens = cu.queries(2, 1, H, 4).cuda(), torch.tensor([[900], [700]], dtype=torch.int32).cuda()
+    want = decode(q, cache, table, lens, SCALE, 4)
+    late, side = torch.ones_like(lens), torch.cuda.Stream()
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        late.copy_(lens)
+    got = decode(q, cache, table, late, SCALE, 4, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
