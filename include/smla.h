@@ -528,7 +528,9 @@ smla_status smla_decode_dense_q4(const void *q, const void *cache_q4, int64_t nu
  *    the attention weight that a decode's query tokens gave to each position:
  *      acc[b, i] += sum over (t, h) with i < seq_lens[b, t] of
  *                   exp(scale * q[b,t,h] . row_i - lse[b,t,h])
- *    for the q, seq_lens and lse of a dense decode over the same cache.  The
+ *    for the q, seq_lens and lse of a dense decode over the same cache.  (The lse of
+ *    a decode over index lists normalises over its list alone: with it, positions
+ *    that the list left out would get weights that nobody gave them.)  The
  *    sum is fp32 in a fixed order: repeated calls give the same bits.
  *      acc  fp32 [B, max_n]  device; positions no query token sees stay as
  *                            they are, and so does a position that no page

@@ -78,10 +78,13 @@ __device__ __forceinline__ float ld_weight(const float *p) {
 // One cluster of CTAs per sequence, each CTA a run of its slots: radix
 // selection of the K-th largest key (digits of 11, 11 and 10 bits, counts
 // summed in the first CTA), bitmaps of the slots above and at it, ties to the
-// smaller slot, then ranks of holes and movers by prefix sums.  A handful of
-// block and cluster barriers with little work between them: latency bounds it.
-// Measured: 8448 slots 17.7 us, 16 sequences of 12132 to 29815 slots 25.0 us
-// (with one CTA a sequence 23.6 and 46.5).
+// smaller slot, then ranks of holes and movers by prefix sums.  Block barriers of
+// 1024 threads with little work between them: their chain bounds it.  Measured:
+// 8448 slots 17.7 us, 16 sequences of 12132 to 29815 slots 25.0 us (with one CTA a
+// sequence 23.6 and 46.5).  Cycles of the first, 34000 in all: keys in 2200,
+// newest position and protected slots 3600, the three digits' counts 900, 560 and 630
+// and their buckets 3600, 3900 and 4100 (about 3000 of each with one CTA to a
+// sequence: the block scan), bitmaps 1100, ranks 8800 (5900), outputs 4700.
 __global__ void __launch_bounds__(kPlanThreads) smla_evict_plan_kernel(const EvictPlanParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int words = p.per / 32;

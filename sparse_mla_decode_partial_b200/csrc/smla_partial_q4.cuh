@@ -25,21 +25,29 @@
 // is a multiplication by a power of two, exact in bf16: P is rounded once.
 // The output is divided by the sum of the rounded P (lse is that of the others),
 // so that a row which dominates is not off by its P's rounding, whatever the
-// list's width or the bound K: one row comes out bit for bit, 64 rows are off by
-// 2.2e-3 of o in place of 2.5e-3 (its own rounding is 1.7e-3), 2048 by 1.93e-3 in
-// place of 1.95e-3.  A product with ones adds them up beside the maxima it is
-// relative to: 111.0 us where the sum of the others takes 108.6 (32 sequences as
-// below; adding up in registers 113.1), 37.1 and 36.8 (64 lists).
+// list's width or the bound K.  One row comes out bit for bit; lists of 513, 1024
+// and 2048 rows whose softmax has a few large weights are off by 1.32e-3, 0.90e-3
+// and 0.61e-3 of o (relative L2) where division by the sum of the others leaves
+// 1.43e-3, 1.08e-3 and 1.20e-3, and o's own rounding is 1.07e-3, 0.75e-3 and
+// 0.53e-3.  A product with ones adds them up, relative to the warp's own maximum:
+// 110.9 us where the sum of the others alone takes 108.5 (32 sequences as below;
+// adding up in registers 113.1), 37.1 and 36.9 (64 lists).
 // Rows 416 bytes apart: the lane-to-row map below keeps every shared load free
 // of bank conflicts without padding, so a page of the cache lands by one bulk
 // copy.
-// What bounds it: per 64-row tile an SM quarter spends about 1090 cycles on its
-// 136 products (eight each) and 970 on the integer half of decoding, and the two
-// hardly overlap: 2080 cycles in all with everything resident, 2450 in a full
-// launch (issue slots 49% taken, integer pipe 43%, tensor pipe 37%, shared memory
-// 42%).  Measured with the combine: 32 sequences of 4329 to 65378 positions, 16
-// heads, 108.5 us (2.4 TB/s of rows; 40 us at the memory's rate); 64 lists of
-// 2048 rows 36.8 us; one list 8.7 us.  Slower: eight warps a tile (137 us for the
+// What bounds it: per 64-row tile an SM quarter spends about 1096 cycles on its
+// 137 products (eight each) and 970 on the integer half of decoding, and the two
+// hardly overlap: 2080 cycles in all in a loop with everything resident.  A full
+// dense launch takes 2730 cycles a tile and SM at 1.6 GHz (issue slots 48% taken,
+// integer pipe 42%, tensor pipe 37%, shared memory 41%) and about 3100 at 1.965
+// GHz: the rest, 0.4 to 0.5 us a tile, does not shrink with the clock, so it is
+// waiting, not issue; for what (pages, or the two barriers a tile) is not known.
+// Lists take about 4200 cycles a tile on the SMs with the most (16 tiles; 40 of
+// 148 SMs have 8): there the warps also issue the rows, 13 cp.async a thread and
+// tile with a division each.  Measured with the combine: 32 sequences of 4329 to
+// 65378 positions, 16 heads, 110.9 us (2.4 TB/s of rows; 40 us at the memory's
+// rate); 64 lists of 2048 rows 37.1 us; one list 8.9 us.  Slower, beside 108.5
+// us with fewer products: eight warps a tile (137 us for the
 // first), one CTA of three groups per SM and a ring of seven pages (124), the
 // score half on tcgen05 with rows decoded into tensor memory (181).
 #pragma once

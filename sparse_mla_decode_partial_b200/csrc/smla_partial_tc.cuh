@@ -76,8 +76,8 @@ constexpr int kMaxTcRows = 64;  // query rows (the MMA's M) of one CTA
 // is 512 (row, group) units and 256 16-byte pieces of rope values, two units
 // per producer thread.  The tensor pipe bounds it as it does bf16 rows: 2.25 us per
 // 64 rows and SM for scores (1.25) and output (1.0).  Measured with the combine:
-// 60 lists of 2048, 64 heads, 48.0 us (120 CTAs of 1024 rows); nine drafts of eight
-// heads over 46089 positions 34.0 us.  Cache rows as M and queries as N: 83 us for the first.
+// 60 lists of 2048, 64 heads, 48.1 us (120 CTAs of 1024 rows); nine drafts of eight
+// heads over 46089 positions 33.6 us.  Cache rows as M and queries as N: 83 us for the first.
 template <bool Q4>
 struct TcCfgT {
     static constexpr int kProducerWarps = Q4 ? 12 : SMLA_TC_PRODUCER_WARPS;

@@ -152,8 +152,10 @@ __device__ __forceinline__ uint32_t q4_code(float x, float inv) {
 // 0-7 also carry its rope values, and the warp finds where the rows go.
 // Every access covers whole 128-byte lines.  1152 bytes in, 416 out per row.
 // Measured, with the read below behind it: 46080 rows of seven prompts 35.2 us
-// (144 MB, 4.1 TB/s, where 6.6 is the most), 64 rows of a decode step 3.7 us.  Memory latency bounds both: issue slots are 57%
-// taken, and 1440 CTAs of eight warps are 1.6 waves.
+// (144 MB, 4.1 TB/s, where 6.6 is the most), 64 rows of a decode step 3.7 us.
+// Memory latency bounds both: issue slots are 58% and 44% taken, and the bytes in
+// flight are what registers hold (69 and 48 a thread).  Rows through shared memory
+// by bulk copies, as the moves of an eviction go, were not tried.
 template <int RPW>
 __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_append_kernel(const Q4AppendParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -302,8 +304,10 @@ __global__ void __launch_bounds__(32 * kQ4Warps) smla_q4_read_kernel(const Q4Rea
 
 // Rows per warp: four keep more loads in flight, once there are rows enough
 // for every SM to hold several such warps; below that, one row per warp has the
-// shorter chain.  (Append and read of 46080 rows: 35.2 us with four, 38.3
-// with one; of 64 rows 5.4 and 3.7.)
+// shorter chain.  (Append + read, us, with one row per warp: 512 rows 1.9 + 1.9,
+// 4736 2.7 + 2.7, 9472 3.9 + 3.6, 14208 5.4 + 4.5, 18944 6.6 + 5.6, 28416 9.3 +
+// 7.4, 46080 14.4 + 11.1; with four: 2.9 + 2.5, 3.1 + 2.5, 4.6 + 4.3, 4.9 + 4.9, 6.4
+// + 5.8, 8.0 + 7.0, 12.3 + 10.1; rows in L2.  18944 is where four begin.)
 __host__ inline bool q4_many_rows(long long rows, int sms) { return rows >= (long long)sms * kQ4Warps * 4 * 4; }
 
 }  // namespace smla

@@ -43,9 +43,11 @@ __device__ __forceinline__ void weigh_row(const WeighParams &a, int b, int r, fl
 // The dense decode's schedule and score product (smla_partial_q4.cuh): CTAs take
 // equal runs of the batch's 64-position tiles, a page lands by one bulk copy,
 // and each warp scores 16 of its rows against the 16 query rows.  Measured: 24
-// sequences of 4635 to 64913 positions, 16 heads, 51.9 us (4.6 TB/s; 36 us at the
-// memory's rate; 70.9 by the kernel below): 0.72 us a page and SM in steady state,
-// 0.6 of it the bytes' time; shared memory is 53% busy.
+// sequences of 4635 to 64913 positions, 16 heads, 58 us on rows that are not in L2
+// (4.0 TB/s; 36 us at the memory's rate), 51 us over and over on the same 236 MB, of
+// which L2 keeps a part (70.9 by the kernel below).  Shared memory is 54% busy,
+// issue slots 46%, the tensor pipe 34%, DRAM 51%: none is full.  Two pages per CTA
+// are in flight, and the next is asked for behind a barrier of the whole CTA.
 struct WeighQ4Cfg {
     static constexpr int kThreads = 128;
     static constexpr int kTile = 64;                       // one page
@@ -158,8 +160,8 @@ __global__ void __launch_bounds__(WeighQ4Cfg::kThreads, WeighQ4Cfg::kMinBlocks)
 // sequences of 4096 positions).
 // Warp 0 rows in, warp 1 TMEM owner and MMA issuer, warps 4-7 epilogue; 4-bit
 // rows: warp 2 queries in, warps 8-15 decode.
-// Measured: 72 query rows over 46089 positions, bf16 16.8 us (8.2 us at the
-// memory's rate, 43 us by mma.sync): 2.4 steps of 128 rows a CTA, so launch,
+// Measured: 72 query rows over 46089 positions, bf16 17.0 us on rows that are not in
+// L2, 15.4 over and over on the same (8.2 us at the memory's rate, 43 us by mma.sync): 2.4 steps of 128 rows a CTA, so launch,
 // queries and the first boxes are half of it; 4-bit 13.8 us (mma.sync in three
 // passes 30.8).  37 sequences of 4096 positions, 4-bit rows: 24 query rows 23.4
 // us, 64 24.7, 72 26.2 (mma.sync with 32, 64, 32 rows a pass: 23.0, 37.2, 63.3);
