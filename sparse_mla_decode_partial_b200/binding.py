@@ -6,6 +6,7 @@ If the library is missing, calls raise -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -159,21 +160,48 @@ def _torch_stream(stream, dev):
     return torch.cuda.ExternalStream(_stream(stream), device=dev)
 
 
-def _new(shape, dtype, dev, stream, returned=True):
-    """An empty tensor that a launch on ``stream`` uses.  It comes from that
-    stream's own memory: a block that the current stream has let go of may still
-    be written by work queued there, which nothing orders before the launch.
-    What is ``returned`` will be read on the current stream, which therefore holds
-    the memory too."""
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=dev)  # (separate sizes parse 0.7 us faster than a tuple)
-    stream = _torch_stream(stream, dev)
-    here = torch.cuda.current_stream(dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(*shape, dtype=dtype, device=dev)
-    if returned and here != stream:
-        t.record_stream(here)
-    return t
+class _Memory:
+    """Allocates the tensors that a launch on ``stream`` uses from that stream's
+    own memory: a block that the current stream has let go of may still be written
+    by work queued there, which nothing orders before the launch.  What is
+    ``returned`` will be read on the current stream, which therefore holds the
+    memory too.  (Streams are compared by handle and switched once per call: a
+    switch costs some 8 us of host time.)"""
+    __slots__ = ("dev", "side", "here", "switch")
+
+    def __init__(self, stream, dev):
+        self.dev, self.here, self.switch = dev, None, None
+        other = stream is not None and _stream(stream) != torch._C._cuda_getCurrentRawStream(dev.index)
+        self.side = _torch_stream(stream, dev) if other else None
+
+    def __enter__(self):
+        return self
+
+    def __call__(self, shape, dtype, returned=True):
+        if self.side is not None and self.switch is None:
+            self.here = torch.cuda.current_stream(self.dev)
+            self.switch = torch.cuda.stream(self.side)
+            self.switch.__enter__()
+        t = torch.empty(*shape, dtype=dtype, device=self.dev)  # (separate sizes parse 0.7 us faster than a tuple)
+        if returned and self.here is not None:
+            t.record_stream(self.here)
+        return t
+
+    def __exit__(self, *exc):
+        if self.switch is not None:
+            self.switch.__exit__(*exc)
+
+
+_plain = {}  # by device: the same for calls without a stream
+
+
+def _memory(stream, dev):
+    if stream is not None:
+        return _Memory(stream, dev)
+    if dev not in _plain:
+        _plain[dev] = contextlib.nullcontext(
+            lambda shape, dtype, returned=True: torch.empty(*shape, dtype=dtype, device=dev))
+    return _plain[dev]
 
 
 def choose_nsplit(B: int, T: int, H: int, K: int, sm_count: int = 0) -> int:
@@ -208,12 +236,13 @@ def decode_partial(q, cache, page_table, idx, scale: float, nsplit: int, *, part
     """Partial pass; returns (part_o [B,T,H,S,512], part_m [B,T,H,S], part_lse [B,T,H,S])."""
     B, T, H, K, pt_stride, num_pages = _decode_args(q, cache, page_table, idx)
     dev = q.device
-    if part_o is None:
-        part_o = _new((B, T, H, nsplit, DC), torch.float32, dev, stream)
-    if part_m is None:
-        part_m = _new((B, T, H, nsplit), torch.float32, dev, stream)
-    if part_lse is None:
-        part_lse = _new((B, T, H, nsplit), torch.float32, dev, stream)
+    with _memory(stream, dev) as new:
+        if part_o is None:
+            part_o = new((B, T, H, nsplit, DC), torch.float32)
+        if part_m is None:
+            part_m = new((B, T, H, nsplit), torch.float32)
+        if part_lse is None:
+            part_lse = new((B, T, H, nsplit), torch.float32)
     _need(part_o, torch.float32, "part_o", dev, (B, T, H, nsplit, DC))
     _need(part_m, torch.float32, "part_m", dev, (B, T, H, nsplit))
     _need(part_lse, torch.float32, "part_lse", dev, (B, T, H, nsplit))
@@ -235,10 +264,11 @@ def lse_combine(part_o, part_m, part_lse, *, o=None, lse=None, stream=None):
     B, T, H, S = part_m.shape
     if tuple(part_o.shape) != (B, T, H, S, DC) or part_lse.shape != part_m.shape:
         raise ValueError("partial shapes disagree")
-    if o is None:
-        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
-    if lse is None:
-        lse = _new((B, T, H), torch.float32, dev, stream)
+    with _memory(stream, dev) as new:
+        if o is None:
+            o = new((B, T, H, DC), torch.bfloat16)
+        if lse is None:
+            lse = new((B, T, H), torch.float32)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_lse_combine(_ptr(part_o), _ptr(part_m), _ptr(part_lse), B, T, H, S, _ptr(o),
@@ -258,13 +288,14 @@ def decode(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, workspac
     if nsplit == 0:
         nsplit = choose_nsplit(B, T, H, K, 0)
     need = workspace_bytes(B, T, H, nsplit) if nsplit > 1 else 0
-    if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
-    _need(workspace, torch.uint8, "workspace", dev)
-    if o is None:
-        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
-    if lse is None:
-        lse = _new((B, T, H), torch.float32, dev, stream)
+    with _memory(stream, dev) as new:
+        if workspace is None:
+            workspace = new((max(need, 16),), torch.uint8, returned=False)
+        _need(workspace, torch.uint8, "workspace", dev)
+        if o is None:
+            o = new((B, T, H, DC), torch.bfloat16)
+        if lse is None:
+            lse = new((B, T, H), torch.float32)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_decode(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
@@ -338,13 +369,14 @@ def decode_dense(q, cache, page_table, seq_lens, scale: float, nsplit: int = 0, 
     if nsplit == 0:
         nsplit = dense_nsplit(B, T, H, K)
     need = dense_workspace_bytes(B, T, H, K, nsplit)
-    if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
-    _need(workspace, torch.uint8, "workspace", dev)
-    if o is None:
-        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
-    if lse is None:
-        lse = _new((B, T, H), torch.float32, dev, stream)
+    with _memory(stream, dev) as new:
+        if workspace is None:
+            workspace = new((max(need, 16),), torch.uint8, returned=False)
+        _need(workspace, torch.uint8, "workspace", dev)
+        if o is None:
+            o = new((B, T, H, DC), torch.bfloat16)
+        if lse is None:
+            lse = new((B, T, H), torch.float32)
     _need(o, torch.bfloat16, "o", dev, (B, T, H, DC))
     _need(lse, torch.float32, "lse", dev, (B, T, H))
     _check(lib().smla_decode_dense(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
@@ -360,12 +392,13 @@ def decode_dense_partial(q, cache, page_table, seq_lens, scale: float, nsplit: i
     part_m [B,T,H,S], part_lse [B,T,H,S])."""
     B, T, H, K, pt_stride, num_pages = _dense_args(q, cache, page_table, seq_lens, K, stream)
     dev = q.device
-    if part_o is None:
-        part_o = _new((B, T, H, nsplit, DC), torch.float32, dev, stream)
-    if part_m is None:
-        part_m = _new((B, T, H, nsplit), torch.float32, dev, stream)
-    if part_lse is None:
-        part_lse = _new((B, T, H, nsplit), torch.float32, dev, stream)
+    with _memory(stream, dev) as new:
+        if part_o is None:
+            part_o = new((B, T, H, nsplit, DC), torch.float32)
+        if part_m is None:
+            part_m = new((B, T, H, nsplit), torch.float32)
+        if part_lse is None:
+            part_lse = new((B, T, H, nsplit), torch.float32)
     _need(part_o, torch.float32, "part_o", dev, (B, T, H, nsplit, DC))
     _need(part_m, torch.float32, "part_m", dev, (B, T, H, nsplit))
     _need(part_lse, torch.float32, "part_lse", dev, (B, T, H, nsplit))
@@ -412,8 +445,9 @@ def decode_host(q, cache, page_table, idx, scale: float, nsplit: int = 0, *, o, 
     if nsplit == 0:
         nsplit = choose_nsplit(B, T, H, K, 0)
     need = workspace_host_bytes(B, T, H, K, pt_stride, nsplit)
-    if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
+    with _memory(stream, dev) as new:
+        if workspace is None:
+            workspace = new((max(need, 16),), torch.uint8, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_decode_host(_ptr(q), _ptr(cache), num_pages, _ptr(page_table), pt_stride,
                                   _ptr(idx), B, T, H, K, PAGE_SIZE, float(scale), int(nsplit),
@@ -460,12 +494,12 @@ def indexer_topk(q_index, w, k_index, page_table, n_vis, K: int, max_n: int, *, 
     B, T, HI, pt_stride, num_pages = _indexer_args(q_index, w, k_index, page_table, n_vis)
     dev = q_index.device
     K = _k_in_range(int(K))
-    if out is None:
-        out = _new((B, T, K), torch.int32, dev, stream)
-    _need(out, torch.int32, "out", dev, (B, T, K))
-    if workspace is None:
-        workspace = _new((max(16, indexer_workspace_bytes(B, T, max_n)),), torch.uint8, dev, stream,
-                         returned=False)
+    with _memory(stream, dev) as new:
+        if out is None:
+            out = new((B, T, K), torch.int32)
+        _need(out, torch.int32, "out", dev, (B, T, K))
+        if workspace is None:
+            workspace = new((max(16, indexer_workspace_bytes(B, T, max_n)),), torch.uint8, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_topk(_ptr(q_index), _ptr(w), _ptr(k_index), num_pages,
                                    _ptr(page_table), pt_stride, _ptr(n_vis), B, T, HI, int(max_n),
@@ -480,15 +514,14 @@ def indexer_scores(q_index, w, k_index, page_table, n_vis, max_n: int, *, scores
     a position is not a candidate; entries past n_vis are not written)."""
     B, T, HI, pt_stride, num_pages = _indexer_args(q_index, w, k_index, page_table, n_vis)
     dev = q_index.device
-    if scores is None:
-        scores = _new((B, T, max(max_n, 1)), torch.float32, dev, stream)
-        with torch.cuda.stream(_torch_stream(stream, dev)):
-            scores.fill_(float("nan"))
-    # rows of max_n scores, one per query token (nothing is written when max_n is 0)
-    _need(scores, torch.float32, "scores", dev, (B, T, max_n) if max_n > 0 else None)
-    if workspace is None:
-        workspace = _new((max(16, indexer_workspace_bytes(B, T, 0)),), torch.uint8, dev, stream,
-                         returned=False)
+    with _memory(stream, dev) as new:
+        if scores is None:
+            scores = new((B, T, max(max_n, 1)), torch.float32)
+            scores.fill_(float("nan"))  # (on the launch's stream, as the allocation)
+        # rows of max_n scores, one per query token (nothing is written when max_n is 0)
+        _need(scores, torch.float32, "scores", dev, (B, T, max_n) if max_n > 0 else None)
+        if workspace is None:
+            workspace = new((max(16, indexer_workspace_bytes(B, T, 0)),), torch.uint8, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_scores(_ptr(q_index), _ptr(w), _ptr(k_index), num_pages,
                                      _ptr(page_table), pt_stride, _ptr(n_vis), B, T, HI,
@@ -506,12 +539,12 @@ def indexer_select(scores, n_vis, K: int, *, out=None, workspace=None, stream=No
     B, T, max_n = scores.shape
     _need(n_vis, torch.int32, "n_vis", dev, (B, T))
     K = _k_in_range(int(K))
-    if out is None:
-        out = _new((B, T, K), torch.int32, dev, stream)
-    _need(out, torch.int32, "out", dev, (B, T, K))
-    if workspace is None:
-        workspace = _new((max(16, indexer_select_workspace_bytes(B, T, max_n)),), torch.uint8, dev, stream,
-                         returned=False)
+    with _memory(stream, dev) as new:
+        if out is None:
+            out = new((B, T, K), torch.int32)
+        _need(out, torch.int32, "out", dev, (B, T, K))
+        if workspace is None:
+            workspace = new((max(16, indexer_select_workspace_bytes(B, T, max_n)),), torch.uint8, returned=False)
     _need(workspace, torch.uint8, "workspace", dev)
     _check(lib().smla_indexer_select(_ptr(scores), _ptr(n_vis), B, T, max_n, int(K),
                                      _ptr(workspace), workspace.numel(), _ptr(out),
@@ -600,10 +633,11 @@ def q4_read(cache, page_table, positions, *, out=None, stream=None):
     _want(positions, torch.int32, "positions", dev)
     B, K = _dims(positions, 2, "positions must be [B, K]")
     num_pages, pt_stride = _paged(cache, Q4_ROW_BYTES, torch.uint8, dev, page_table, B)
-    if out is None:
-        out = _new((B, K, D), torch.bfloat16, dev, stream)
-    else:
-        _want(out, torch.bfloat16, "out", dev, (B, K, D))
+    with _memory(stream, dev) as new:
+        if out is None:
+            out = new((B, K, D), torch.bfloat16)
+        else:
+            _want(out, torch.bfloat16, "out", dev, (B, K, D))
     _launch("smla_q4_read", dev, stream, cache.data_ptr(), num_pages, page_table.data_ptr(), pt_stride,
             positions.data_ptr(), B, _k_in_range(K), PAGE_SIZE, out.data_ptr())
     return out
@@ -636,18 +670,19 @@ def _queries(q):
 
 def _decode_out(dev, B, T, H, need, workspace, o, lse, stream):
     """Workspace and outputs of a decode, allocated where they are not given."""
-    if workspace is None:
-        workspace = _new((max(need, 16),), torch.uint8, dev, stream, returned=False)
-    else:
-        _want(workspace, torch.uint8, "workspace", dev)
-    if o is None:
-        o = _new((B, T, H, DC), torch.bfloat16, dev, stream)
-    else:
-        _want(o, torch.bfloat16, "o", dev, (B, T, H, DC))
-    if lse is None:
-        lse = _new((B, T, H), torch.float32, dev, stream)
-    else:
-        _want(lse, torch.float32, "lse", dev, (B, T, H))
+    with _memory(stream, dev) as new:
+        if workspace is None:
+            workspace = new((max(need, 16),), torch.uint8, returned=False)
+        else:
+            _want(workspace, torch.uint8, "workspace", dev)
+        if o is None:
+            o = new((B, T, H, DC), torch.bfloat16)
+        else:
+            _want(o, torch.bfloat16, "o", dev, (B, T, H, DC))
+        if lse is None:
+            lse = new((B, T, H), torch.float32)
+        else:
+            _want(lse, torch.float32, "lse", dev, (B, T, H))
     return workspace, o, lse
 
 
@@ -745,22 +780,23 @@ def evict_plan(acc, n, K: int, *, pos=None, n_sink: int = 0, n_recent: int = 0, 
     _want(n, torch.int32, "n", dev, (B,))
     if pos is not None:
         _want(pos, torch.int32, "pos", dev, (B, max_n))
-    if src is None:
-        src = _new((B, K), torch.int32, dev, stream)
-    else:
-        _want(src, torch.int32, "src", dev, (B, K))
-    if n_new is None:
-        n_new = _new((B,), torch.int32, dev, stream)
-    else:
-        _want(n_new, torch.int32, "n_new", dev, (B,))
-    if acc_new is None:
-        acc_new = _new((B, max_n), torch.float32, dev, stream)
-    else:
-        _want(acc_new, torch.float32, "acc_new", dev, (B, max_n))
-    if pos_new is None:
-        pos_new = _new((B, max_n), torch.int32, dev, stream)
-    else:
-        _want(pos_new, torch.int32, "pos_new", dev, (B, max_n))
+    with _memory(stream, dev) as new:
+        if src is None:
+            src = new((B, K), torch.int32)
+        else:
+            _want(src, torch.int32, "src", dev, (B, K))
+        if n_new is None:
+            n_new = new((B,), torch.int32)
+        else:
+            _want(n_new, torch.int32, "n_new", dev, (B,))
+        if acc_new is None:
+            acc_new = new((B, max_n), torch.float32)
+        else:
+            _want(acc_new, torch.float32, "acc_new", dev, (B, max_n))
+        if pos_new is None:
+            pos_new = new((B, max_n), torch.int32)
+        else:
+            _want(pos_new, torch.int32, "pos_new", dev, (B, max_n))
     _launch("smla_evict_plan", dev, stream, acc.data_ptr(), None if pos is None else pos.data_ptr(),
             n.data_ptr(), B, max_n, K, n_sink, n_recent, None, 0, src.data_ptr(), n_new.data_ptr(),
             acc_new.data_ptr(), pos_new.data_ptr())
